@@ -101,6 +101,7 @@ typedef enum { TB_MASK_PER_HEAD = 0, TB_MASK_SHARED = 1, TB_MASK_DENSE = 2, TB_M
 #define TB_DEV_ERR_INDEX 0x1u     /* a gathered index was outside [0, len)    */
 #define TB_DEV_ERR_COUNT 0x2u     /* a selected-set size differed from k      */
 #define TB_DEV_ERR_TIMEOUT 0x4u   /* a bounded wait gave up                   */
+#define TB_DEV_ERR_VALUE 0x8u     /* a NaN or an infinity was written to an 8-bit cache */
 
 #define TB_MAX_BATCH 128
 #define TB_MAX_LAYERS 64
@@ -157,6 +158,67 @@ TB_API tb_status tb_bind_layer(tb_ctx* ctx, int layer, void* k_cache, void* v_ca
 TB_API tb_status tb_bind_layer_paged(tb_ctx* ctx, int layer, void* k_pool, void* v_pool, int num_pages,
                                      const int32_t* page_table, int page_size, int max_pages, void* kimp_cache,
                                      const void* w_k);
+
+/* ---- 8-bit K/V caches --------------------------------------------------
+ * Beyond the pages, which keep the cache's precision: a layer may hold K and
+ * V as one byte an element, half the bytes of bf16 for every row that the
+ * attention and the soft votes read.  One fp32 scale serves an aligned block
+ * of TB_KV8_BLOCK tokens of one (sequence, KV head), for K and for V:
+ *
+ *   scale = 2^e, e = max(-100, smallest integer with amax <= F 2^e)
+ *   code  = x / scale rounded to nearest, ties to even
+ *
+ * with amax the largest finite magnitude of the block's rows and F the
+ * format's largest value: TB_KV8_E4M3 (1 sign, 4 exponent, 3 mantissa bits,
+ * F = 448; small values keep their relative precision) or TB_KV8_INT8 (codes
+ * -127..127, F = 127; finer where a block's values are of one size).  When a
+ * token joins a block that holds rows already, e is the larger of its old
+ * value and the new rows' own, and the older codes are rounded again if it
+ * grew; tb_set_seq_lens back into a block keeps its scale.  An infinity is
+ * stored as the largest value of its block, a NaN as zero; either sets
+ * TB_DEV_ERR_VALUE.  The e4m3 codes 0x7F and 0xFF (NaN) are never written and
+ * must not be put there.
+ *   k_codes, v_codes   [B][Hkv][max_len][D]               1 byte
+ *   k_scale, v_scale   [B][Hkv][max_len/TB_KV8_BLOCK]     fp32
+ * New rows, queries, outputs and W_K keep kv_dtype.  Rows are written by
+ * tb_append_kv / tb_decode_step (one token) and tb_append_kv_rows, all of which
+ * form K_imp from the unrounded keys, so that selections do not depend on the
+ * cache's format; tb_project_kimp recomputes K_imp from the codes (fp32 FMA).
+ * Every call works on such layers, and a context may mix them with others.
+ * Lengths start at 0. */
+#define TB_KV8_BLOCK 16
+typedef enum { TB_KV8_E4M3 = 1, TB_KV8_INT8 = 2 } tb_kv8_format;
+TB_API tb_status tb_bind_layer_kv8(tb_ctx* ctx, int layer, int format, void* k_codes, void* v_codes, float* k_scale,
+                                   float* v_scale, void* kimp_cache, const void* w_k);
+
+/* The same with paged caches: code pools [num_pages][Hkv][page_size][D], scale
+ * pools [num_pages][Hkv][page_size/TB_KV8_BLOCK], and the page table of
+ * tb_bind_layer_paged (same limits).  A page's scales move with it.  A page
+ * may be shared by sequences that only read it: the block a sequence appends
+ * into must be its own.  A page id outside [0, num_pages) sets
+ * TB_DEV_ERR_INDEX; its tokens are not written, not read back, left out of
+ * the attention and the votes, and project to zero. */
+TB_API tb_status tb_bind_layer_kv8_paged(tb_ctx* ctx, int layer, int format, void* k_pool, void* v_pool,
+                                         float* k_scale, float* v_scale, int num_pages, const int32_t* page_table,
+                                         int page_size, int max_pages, void* kimp_cache, const void* w_k);
+
+/* Appends counts_host[b] >= 0 tokens to every sequence b of an 8-bit layer (a
+ * prompt, or a chunk of one): quantises K and V, forms K_imp from the
+ * unrounded keys in fp32 accumulation, and adds counts_host[b] to len[b]
+ * (host-side, at enqueue time).  Element (b, g, i, d) of K is
+ * k[b*k_strides[0] + g*k_strides[1] + i*k_strides[2] + d] (kv_dtype, strides
+ * in elements), V likewise; k, v and every stride must be multiples of 16
+ * bytes (TB_ERR_SHAPE).  Rows past counts_host[b] are not read, and cache rows
+ * past the new length keep their codes.  TB_ERR_CAPACITY if a sequence
+ * would exceed max_len; TB_ERR_UNSUPPORTED for a layer that is not 8-bit. */
+TB_API tb_status tb_append_kv_rows(tb_ctx* ctx, int layer, const void* k, const void* v,
+                                   const int64_t k_strides[3], const int64_t v_strides[3],
+                                   const int32_t* counts_host, void* stream);
+
+/* Reads rows [start, start + count) of every (b, KV head) of an 8-bit layer
+ * back as code * scale: k_out, v_out [B][Hkv][count][D] kv_dtype (either may
+ * be NULL, not both; exact in bf16 and fp32).  Rows t >= len[b] are left untouched. */
+TB_API tb_status tb_read_kv(tb_ctx* ctx, int layer, int start, int count, void* k_out, void* v_out, void* stream);
 
 /* Set / read the per-sequence lengths of a layer (host arrays of `batch`
  * int32).  Used after the caller filled the caches by a prefill. */

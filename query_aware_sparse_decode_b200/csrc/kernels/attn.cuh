@@ -44,14 +44,14 @@ struct AttnParams {
   int lens[kMaxBatch];
 };
 
-// Builds the CTA's gather list: the cache rows of the ascending union tokens
-// of [t0, t1) (at most kAttnMaxChunk tokens, 64 mask words) with a head
-// bitmask each; pads to a multiple of 16 with (row of t0, no head).  Warps 0
-// and 1 read the words (one per lane) and scan their counts; then each thread
-// expands half a word (16 tokens).
-template <int GS>
-__device__ __forceinline__ int build_union_list(const AttnParams& p, int b, int g, int t0, int t1, int32_t* list_idx,
-                                                uint8_t* list_hb, uint32_t* scan_sm) {
+// Lists the union tokens of [t0, t1) (at most kAttnMaxChunk tokens, 64 mask
+// words) in ascending order: put(position, token, head bits) for each, and up
+// to a multiple of 16 positions put(position, t0, 0).  Returns their number
+// (without the padding).  Warps 0 and 1 read the words (one per lane) and scan
+// their counts; then each thread expands half a word (16 tokens).
+template <int GS, class Put>
+__device__ __forceinline__ int build_union(const AttnParams& p, int b, int g, int t0, int t1, uint32_t* scan_sm,
+                                           Put put) {
   constexpr int NWM = kAttnMaxChunk / 32;
   static_assert(NWM <= 64 && kAttnThreads == 2 * NWM, "two warps hold the words; a thread expands half a word");
   __shared__ uint32_t s_u[NWM], s_excl[NWM], s_hm[GS][NWM];
@@ -111,19 +111,25 @@ __device__ __forceinline__ int build_union_list(const AttnParams& p, int b, int 
 #pragma unroll
           for (int hh = 0; hh < GS; ++hh) hb |= ((s_hm[hh][w] >> j) & 1u) << hh;
         }
-        list_idx[pos] = (int32_t)kv_row(p.kl, b, g, p.Hkv, p.max_len, t0 + 32 * w + j);  // the token's cache row
-        list_hb[pos] = (uint8_t)hb;
+        put(pos, t0 + 32 * w + j, hb);
         ++pos;
       }
     }
   }
   const int padded = (total + kAttnTile - 1) / kAttnTile * kAttnTile;
-  for (int i = total + tid; i < padded; i += kAttnThreads) {
-    list_idx[i] = (int32_t)kv_row(p.kl, b, g, p.Hkv, p.max_len, t0);
-    list_hb[i] = 0;
-  }
+  for (int i = total + tid; i < padded; i += kAttnThreads) put(i, t0, 0u);
   __syncthreads();
   return total;
+}
+
+// The CTA's gather list: the cache row and the head bitmask of every union token.
+template <int GS>
+__device__ __forceinline__ int build_union_list(const AttnParams& p, int b, int g, int t0, int t1, int32_t* list_idx,
+                                                uint8_t* list_hb, uint32_t* scan_sm) {
+  return build_union<GS>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
+    list_idx[pos] = (int32_t)kv_row(p.kl, b, g, p.Hkv, p.max_len, t);
+    list_hb[pos] = (uint8_t)hb;
+  });
 }
 
 // Writes the CTA's merged (m, l, o) partial for each head of the group from

@@ -33,11 +33,25 @@ constexpr float kNegInf = -__builtin_huge_valf();
 struct KvLayout {
   const int32_t* page_table;  // null: dense
   int page_size, page_shift, max_pages;
+  int num_pages;              // pages of the pool (0 for dense caches)
 };
 __device__ __forceinline__ uint32_t kv_row(const KvLayout& kl, int b, int g, int Hkv, int max_len, int t) {
   if (kl.page_table == nullptr) return ((uint32_t)b * Hkv + g) * (uint32_t)max_len + (uint32_t)t;
   const int page = kl.page_table[(size_t)b * kl.max_pages + (t >> kl.page_shift)];
   return ((uint32_t)page * Hkv + g) * (uint32_t)kl.page_size + (uint32_t)(t & (kl.page_size - 1));
+}
+// kv_row with the page id checked against the pool; false: not a page of it.
+__host__ __device__ __forceinline__ bool kv_row_checked(const KvLayout& kl, int b, int g, int Hkv, int max_len,
+                                                        int t, uint32_t* row) {
+  if (kl.page_table == nullptr) {
+    *row = ((uint32_t)b * Hkv + g) * (uint32_t)max_len + (uint32_t)t;
+    return true;
+  }
+  const int page = kl.page_table[(size_t)b * kl.max_pages + (t >> kl.page_shift)];
+  *row = 0u;
+  if ((unsigned)page >= (unsigned)kl.num_pages) return false;
+  *row = ((uint32_t)page * Hkv + g) * (uint32_t)kl.page_size + (uint32_t)(t & (kl.page_size - 1));
+  return true;
 }
 
 

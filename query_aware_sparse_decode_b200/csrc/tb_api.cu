@@ -11,11 +11,13 @@
 #include <new>
 
 #include "kernels/attn.cuh"
+#include "kernels/attn_kv8.cuh"
 #include "kernels/attn_split.cuh"
 #include "kernels/combine.cuh"
 #include "kernels/index_mask.cuh"
 #include "kernels/common.cuh"
 #include "kernels/kimp.cuh"
+#include "kernels/kv8.cuh"
 #include "kernels/prefill.cuh"
 #include "kernels/reuse.cuh"
 #include "kernels/project_tc.cuh"
@@ -39,6 +41,9 @@ struct LayerState {
   CUtensorMap k_map;  // bf16 caches: K rows, 64-column boxes of 128 rows, 128B swizzle
   int lens[TB_MAX_BATCH];
   KvLayout kl{};       // dense (page_table null) or paged K/V caches
+  int kv8 = 0;         // 0: kv_dtype caches, else the tb_kv8_format of an 8-bit cache
+  float* k_scale = nullptr;  // 8-bit caches: one scale per TB_KV8_BLOCK cache rows
+  float* v_scale = nullptr;
   // selection cache (amortised selection), caller-owned, or null
   float* sc_q = nullptr;        // [B*rows][d'] importance query of the cached set
   int32_t* sc_len = nullptr;    // [B*rows] length at which it was selected (0: empty)
@@ -394,6 +399,36 @@ static tb_status launch_select(tb_ctx* ctx, int layer, const float* scores, bool
   return s;
 }
 
+// The split attention kernel over an 8-bit layer (the partials' combine is the caller's).
+static tb_status launch_attn_kv8(const tb_ctx* ctx, const LayerState& ls, const AttnParams& base, dim3 grid,
+                                 cudaStream_t st) {
+  const tb_config& c = ctx->cfg;
+  const int gs = c.n_q_heads / c.n_kv_heads;
+  AttnKv8Params p{};
+  static_cast<AttnParams&>(p) = base;
+  p.k_scale = ls.k_scale;
+  p.v_scale = ls.v_scale;
+#define TB_KV8_CASE(T, F, DV, GSV)                                                                   \
+  if (ls.kv8 == F && c.head_dim == DV && gs == GSV) {                                                \
+    auto k = attn_kv8_fma_kernel<T, F, DV, GSV>;                                                     \
+    const int smem = attn_kv8_fma_smem<DV, GSV>();                                                   \
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)   \
+      return TB_ERR_CUDA;                                                                            \
+    launch_pdl(k, grid, dim3(kAttnThreads), smem, st, p);                                            \
+  } else
+#define TB_KV8_CASES(T, F)                                                                                        \
+  TB_KV8_CASE(T, F, 128, 4) TB_KV8_CASE(T, F, 128, 2) TB_KV8_CASE(T, F, 128, 1) TB_KV8_CASE(T, F, 128, 8)   \
+  TB_KV8_CASE(T, F, 64, 4) TB_KV8_CASE(T, F, 64, 2) TB_KV8_CASE(T, F, 64, 1) TB_KV8_CASE(T, F, 64, 8)
+  if (c.kv_dtype == TB_BF16) {
+    TB_KV8_CASES(__nv_bfloat16, TB_KV8_E4M3) TB_KV8_CASES(__nv_bfloat16, TB_KV8_INT8) return TB_ERR_UNSUPPORTED;
+  } else {
+    TB_KV8_CASES(float, TB_KV8_E4M3) TB_KV8_CASES(float, TB_KV8_INT8) return TB_ERR_UNSUPPORTED;
+  }
+#undef TB_KV8_CASES
+#undef TB_KV8_CASE
+  return cuda_status(cudaGetLastError());
+}
+
 static tb_status launch_attn(tb_ctx* ctx, int layer, const void* q, const uint32_t* mask, int mode, void* out,
                              float* lse, cudaStream_t st, bool out_f32 = false) {
   const tb_config& c = ctx->cfg;
@@ -422,6 +457,10 @@ static tb_status launch_attn(tb_ctx* ctx, int layer, const void* q, const uint32
   if (p.nsplit > ctx->lay.max_splits) return TB_ERR_WORKSPACE;
   {
     dim3 grid(p.nsplit, c.n_kv_heads, c.batch);
+    if (ls.kv8) {
+      const tb_status s8 = launch_attn_kv8(ctx, ls, p, grid, st);
+      if (s8 != TB_OK) return s8;
+    } else
 #define TB_ATTN_CASE(DV, GSV)                                                                               \
   if (c.head_dim == DV && gs == GSV) {                                                                      \
     if (c.kv_dtype == TB_BF16) {                                                                            \
@@ -505,6 +544,20 @@ static tb_status launch_softvote(tb_ctx* ctx, int layer, const void* q, float* v
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
   for (int b = 0; b < c.batch; ++b) p.lens[b] = ls.lens[b];
   dim3 grid((maxL + p.chunk - 1) / p.chunk, c.n_kv_heads, c.batch);
+  VoteKv8Params p8{};
+  static_cast<VoteParams&>(p8) = p;
+  p8.k_scale = ls.k_scale;
+  p8.status = ctx->status;
+#define TB_VOTE8_CASE(F, DV, GSV)                                                             \
+  if (ls.kv8 == F && c.head_dim == DV && gs == GSV)                                           \
+    launch_pdl(softvote_kv8_logits_kernel<F, DV, GSV>, grid, dim3(kVoteThreads), 0, st, p8);  \
+  else
+#define TB_VOTE8_CASES(F)                                                                                   \
+  TB_VOTE8_CASE(F, 128, 4) TB_VOTE8_CASE(F, 128, 2) TB_VOTE8_CASE(F, 128, 1) TB_VOTE8_CASE(F, 128, 8)   \
+  TB_VOTE8_CASE(F, 64, 4) TB_VOTE8_CASE(F, 64, 2) TB_VOTE8_CASE(F, 64, 1) TB_VOTE8_CASE(F, 64, 8)
+  TB_VOTE8_CASES(TB_KV8_E4M3) TB_VOTE8_CASES(TB_KV8_INT8)
+#undef TB_VOTE8_CASES
+#undef TB_VOTE8_CASE
 #define TB_VOTE_CASE(DV, GSV)                                                                 \
   if (c.head_dim == DV && gs == GSV) {                                                        \
     auto k = softvote_logits_kernel<DV, GSV>;                                                 \
@@ -604,6 +657,7 @@ TB_API tb_status tb_bind_layer(tb_ctx* ctx, int layer, void* k_cache, void* v_ca
   ls.kimp = kimp_cache;
   ls.wk = w_k;
   ls.kl = KvLayout{};
+  ls.kv8 = 0;
   std::memset(ls.lens, 0, sizeof(ls.lens));
   ls.bound = true;
   return TB_OK;
@@ -626,10 +680,52 @@ TB_API tb_status tb_bind_layer_paged(tb_ctx* ctx, int layer, void* k_pool, void*
   ls.v = v_pool;
   ls.kimp = kimp_cache;
   ls.wk = w_k;
-  ls.kl = KvLayout{page_table, page_size, shift, max_pages};
+  ls.kl = KvLayout{page_table, page_size, shift, max_pages, num_pages};
+  ls.kv8 = 0;
   std::memset(ls.lens, 0, sizeof(ls.lens));
   ls.bound = true;
   return TB_OK;
+}
+
+static tb_status bind_kv8(tb_ctx* ctx, int layer, int format, void* k, void* v, float* k_scale, float* v_scale,
+                          const KvLayout& kl, void* kimp, const void* w_k) {
+  if (format != TB_KV8_E4M3 && format != TB_KV8_INT8) return TB_ERR_INVALID_ARG;
+  if (!k || !v || !k_scale || !v_scale || !kimp || !w_k) return TB_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned16(kimp) ||
+      !aligned16(w_k))
+    return TB_ERR_SHAPE;
+  LayerState& ls = ctx->layers[layer];
+  ls.k = k;
+  ls.v = v;
+  ls.k_scale = k_scale;
+  ls.v_scale = v_scale;
+  ls.kimp = kimp;
+  ls.wk = w_k;
+  ls.kl = kl;
+  ls.kv8 = format;
+  std::memset(ls.lens, 0, sizeof(ls.lens));
+  ls.bound = true;
+  return TB_OK;
+}
+
+TB_API tb_status tb_bind_layer_kv8(tb_ctx* ctx, int layer, int format, void* k_codes, void* v_codes, float* k_scale,
+                                   float* v_scale, void* kimp_cache, const void* w_k) {
+  if (!ctx || layer < 0 || layer >= ctx->cfg.n_layers) return TB_ERR_INVALID_ARG;
+  return bind_kv8(ctx, layer, format, k_codes, v_codes, k_scale, v_scale, KvLayout{}, kimp_cache, w_k);
+}
+
+TB_API tb_status tb_bind_layer_kv8_paged(tb_ctx* ctx, int layer, int format, void* k_pool, void* v_pool,
+                                         float* k_scale, float* v_scale, int num_pages, const int32_t* page_table,
+                                         int page_size, int max_pages, void* kimp_cache, const void* w_k) {
+  if (!ctx || layer < 0 || layer >= ctx->cfg.n_layers || !page_table) return TB_ERR_INVALID_ARG;
+  const tb_config& c = ctx->cfg;
+  if (page_size < 16 || (page_size & (page_size - 1)) != 0 || num_pages < 1 || max_pages < 1) return TB_ERR_SHAPE;
+  if ((long long)max_pages * page_size < c.max_len) return TB_ERR_SHAPE;
+  if ((long long)num_pages * c.n_kv_heads * page_size >= (1LL << 31)) return TB_ERR_SHAPE;
+  int shift = 0;
+  while ((1 << shift) < page_size) ++shift;
+  return bind_kv8(ctx, layer, format, k_pool, v_pool, k_scale, v_scale,
+                  KvLayout{page_table, page_size, shift, max_pages, num_pages}, kimp_cache, w_k);
 }
 
 TB_API tb_status tb_set_seq_lens(tb_ctx* ctx, int layer, const int32_t* lens_host) {
@@ -747,11 +843,143 @@ static tb_status append_params(const tb_ctx* ctx, int layer, const void* k_new, 
   return TB_OK;
 }
 
+// Quantised write of cnt[b] rows behind every sequence of an 8-bit layer; the
+// layer's lengths grow by cnt[b] once the kernel is enqueued.
+static tb_status launch_kv8_write(tb_ctx* ctx, int layer, const void* k, const void* v, const int64_t* ks,
+                                  const int64_t* vs, const int32_t* cnt, cudaStream_t st) {
+  const tb_config& c = ctx->cfg;
+  LayerState& ls = ctx->layers[layer];
+  Kv8WriteParams p{};
+  p.src[0] = k;
+  p.src[1] = v;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t* s = i ? vs : ks;
+    p.sb[i] = s[0];
+    p.sh[i] = s[1];
+    p.st[i] = s[2];
+  }
+  p.codes[0] = static_cast<uint8_t*>(ls.k);
+  p.codes[1] = static_cast<uint8_t*>(ls.v);
+  p.scale[0] = ls.k_scale;
+  p.scale[1] = ls.v_scale;
+  p.kimp = ls.kimp;
+  p.w_k = ls.wk;
+  p.status = ctx->status;
+  p.kl = ls.kl;
+  p.Hkv = c.n_kv_heads;
+  p.dimp = c.d_imp;
+  p.max_len = c.max_len;
+  p.kimp_bf16 = c.kimp_bf16;
+  int blocks = 0;  // most blocks that one sequence's new rows touch
+  for (int b = 0; b < c.batch; ++b) {
+    if (cnt[b] < 0) return TB_ERR_INVALID_ARG;
+    if ((long long)ls.lens[b] + cnt[b] > c.max_len) return TB_ERR_CAPACITY;
+    p.pos[b] = ls.lens[b];
+    p.cnt[b] = cnt[b];
+    if (cnt[b] > 0)
+      blocks = std::max(blocks, (ls.lens[b] % kKv8Block + cnt[b] + kKv8Block - 1) / kKv8Block);
+  }
+  if (blocks == 0) return TB_OK;
+  const dim3 grid((unsigned)blocks, c.n_kv_heads, c.batch);
+#define TB_KV8_WRITE(T, F, DV)                                                      \
+  if (ls.kv8 == F && c.head_dim == DV)                                              \
+    launch_pdl(kv8_write_kernel<T, F, DV>, grid, dim3(kKv8WriteThreads), 0, st, p); \
+  else
+#define TB_KV8_WRITES(T)                                                                                   \
+  TB_KV8_WRITE(T, TB_KV8_E4M3, 128) TB_KV8_WRITE(T, TB_KV8_E4M3, 64) TB_KV8_WRITE(T, TB_KV8_INT8, 128) \
+  TB_KV8_WRITE(T, TB_KV8_INT8, 64) return TB_ERR_UNSUPPORTED;
+  if (c.kv_dtype == TB_BF16) {
+    TB_KV8_WRITES(__nv_bfloat16)
+  } else {
+    TB_KV8_WRITES(float)
+  }
+#undef TB_KV8_WRITES
+#undef TB_KV8_WRITE
+  ++ctx->launches;
+  const tb_status s = cuda_status(cudaGetLastError());
+  if (s != TB_OK) return s;
+  for (int b = 0; b < c.batch; ++b) ls.lens[b] += cnt[b];
+  return TB_OK;
+}
+
+// The context's device must be current: kernels and streams are its own.
+static bool on_device(const tb_ctx* ctx) {
+  int d = -1;
+  return cudaGetDevice(&d) == cudaSuccess && d == ctx->device;
+}
+
+TB_API tb_status tb_append_kv_rows(tb_ctx* ctx, int layer, const void* k, const void* v, const int64_t k_strides[3],
+                                   const int64_t v_strides[3], const int32_t* counts_host, void* stream) {
+  const tb_status s = check_layer(ctx, layer);
+  if (s != TB_OK) return s;
+  if (!ctx->layers[layer].kv8) return TB_ERR_UNSUPPORTED;
+  if (!k || !v || !k_strides || !v_strides || !counts_host) return TB_ERR_INVALID_ARG;
+  const int per16 = ctx->cfg.kv_dtype == TB_BF16 ? 8 : 4;  // elements of 16 bytes
+  if (!aligned16(k) || !aligned16(v)) return TB_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (k_strides[i] % per16 || v_strides[i] % per16) return TB_ERR_SHAPE;
+  if (!on_device(ctx)) return TB_ERR_INVALID_ARG;
+  return launch_kv8_write(ctx, layer, k, v, k_strides, v_strides, counts_host, static_cast<cudaStream_t>(stream));
+}
+
+TB_API tb_status tb_read_kv(tb_ctx* ctx, int layer, int start, int count, void* k_out, void* v_out, void* stream) {
+  const tb_status s = check_layer(ctx, layer);
+  if (s != TB_OK) return s;
+  const tb_config& c = ctx->cfg;
+  const LayerState& ls = ctx->layers[layer];
+  if (!ls.kv8) return TB_ERR_UNSUPPORTED;
+  if ((!k_out && !v_out) || start < 0 || count < 0) return TB_ERR_INVALID_ARG;
+  if ((long long)start + count > c.max_len) return TB_ERR_CAPACITY;
+  if (!aligned16(k_out) || !aligned16(v_out)) return TB_ERR_SHAPE;
+  if (!on_device(ctx)) return TB_ERR_INVALID_ARG;
+  Kv8ReadParams p{};
+  p.codes[0] = static_cast<const uint8_t*>(ls.k);
+  p.codes[1] = static_cast<const uint8_t*>(ls.v);
+  p.scale[0] = ls.k_scale;
+  p.scale[1] = ls.v_scale;
+  p.out[0] = k_out;
+  p.out[1] = v_out;
+  p.status = ctx->status;
+  p.kl = ls.kl;
+  p.Hkv = c.n_kv_heads;
+  p.max_len = c.max_len;
+  p.start = start;
+  p.count = count;
+  for (int b = 0; b < c.batch; ++b) p.lens[b] = ls.lens[b];
+  const int n = std::min(count, max_len_of(ls, c.batch) - start);  // rows that some sequence holds
+  if (n <= 0) return TB_OK;
+  const dim3 grid((unsigned)(((long long)n * (c.head_dim / 16) + 255) / 256), c.n_kv_heads, c.batch);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define TB_KV8_READ(T, F, DV)                                         \
+  if (ls.kv8 == F && c.head_dim == DV)                                \
+    launch_pdl(kv8_read_kernel<T, F, DV>, grid, dim3(256), 0, st, p); \
+  else
+#define TB_KV8_READS(T)                                                                                 \
+  TB_KV8_READ(T, TB_KV8_E4M3, 128) TB_KV8_READ(T, TB_KV8_E4M3, 64) TB_KV8_READ(T, TB_KV8_INT8, 128) \
+  TB_KV8_READ(T, TB_KV8_INT8, 64) return TB_ERR_UNSUPPORTED;
+  if (c.kv_dtype == TB_BF16) {
+    TB_KV8_READS(__nv_bfloat16)
+  } else {
+    TB_KV8_READS(float)
+  }
+#undef TB_KV8_READS
+#undef TB_KV8_READ
+  ++ctx->launches;
+  return cuda_status(cudaGetLastError());
+}
+
 TB_API tb_status tb_append_kv(tb_ctx* ctx, int layer, const void* k_new, const void* v_new, void* stream) {
   tb_status s = check_layer(ctx, layer);
   if (s != TB_OK) return s;
   const tb_config& c = ctx->cfg;
   LayerState& ls = ctx->layers[layer];
+  if (ls.kv8) {  // one row a sequence, [B][Hkv][D]
+    if (!k_new || !v_new) return TB_ERR_INVALID_ARG;
+    const int64_t strides[3] = {(int64_t)c.n_kv_heads * c.head_dim, c.head_dim, c.head_dim};
+    int32_t one[TB_MAX_BATCH];
+    std::fill(one, one + c.batch, 1);
+    return launch_kv8_write(ctx, layer, k_new, v_new, strides, strides, one, static_cast<cudaStream_t>(stream));
+  }
   AppendParams p;
   s = append_params(ctx, layer, k_new, v_new, &p);
   if (s != TB_OK) return s;
@@ -766,6 +994,32 @@ TB_API tb_status tb_append_kv(tb_ctx* ctx, int layer, const void* k_new, const v
   if (s != TB_OK) return s;
   for (int b = 0; b < c.batch; ++b) ls.lens[b] += 1;
   return TB_OK;
+}
+
+// K_imp rows [start, start + count) of an 8-bit layer from its codes.
+static tb_status launch_kv8_project(tb_ctx* ctx, int layer, int start, int count, cudaStream_t st) {
+  const tb_config& c = ctx->cfg;
+  const LayerState& ls = ctx->layers[layer];
+  const Kv8ProjectParams p{static_cast<const uint8_t*>(ls.k), ls.k_scale, ls.kimp, ls.wk, ctx->status, ls.kl,
+                           c.n_kv_heads, c.max_len, start, count, c.kimp_bf16};
+  const dim3 grid((count + 31) / 32, c.n_kv_heads, c.batch);
+#define TB_KV8_PROJ(T, F, DV, DI)                                   \
+  if (ls.kv8 == F && c.head_dim == DV && c.d_imp == DI)             \
+    kv8_project_kernel<T, F, DV, DI><<<grid, 256, 0, st>>>(p);      \
+  else
+#define TB_KV8_PROJS(T)                                                                                      \
+  TB_KV8_PROJ(T, TB_KV8_E4M3, 128, 32) TB_KV8_PROJ(T, TB_KV8_E4M3, 128, 16) TB_KV8_PROJ(T, TB_KV8_E4M3, 64, 32) \
+  TB_KV8_PROJ(T, TB_KV8_E4M3, 64, 16) TB_KV8_PROJ(T, TB_KV8_INT8, 128, 32) TB_KV8_PROJ(T, TB_KV8_INT8, 128, 16) \
+  TB_KV8_PROJ(T, TB_KV8_INT8, 64, 32) TB_KV8_PROJ(T, TB_KV8_INT8, 64, 16) return TB_ERR_UNSUPPORTED;
+  if (c.kv_dtype == TB_BF16) {
+    TB_KV8_PROJS(__nv_bfloat16)
+  } else {
+    TB_KV8_PROJS(float)
+  }
+#undef TB_KV8_PROJS
+#undef TB_KV8_PROJ
+  ++ctx->launches;
+  return cuda_status(cudaGetLastError());
 }
 
 // One persistent tcgen05 launch projecting rows [start, start + count) of
@@ -811,6 +1065,7 @@ TB_API tb_status tb_project_kimp(tb_ctx* ctx, int layer, int start, int count, v
   if (count == 0) return TB_OK;
   const LayerState& ls = ctx->layers[layer];
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (ls.kv8) return launch_kv8_project(ctx, layer, start, count, st);
   if (c.kv_dtype == TB_BF16 && ls.kl.page_table == nullptr) return launch_project_tc(ctx, layer, 1, start, count, st);
   // fp32 caches, and paged caches of either type (a TMA tile may not cross pages): fp32 FMA
   ProjectParams p{ls.k, ls.kimp, ls.wk, c.n_kv_heads, c.max_len, start, count, ls.kl, c.kimp_bf16};
@@ -839,10 +1094,10 @@ TB_API tb_status tb_project_kimp_layers(tb_ctx* ctx, int first_layer, int n_laye
   for (int l = first_layer; l < first_layer + n_layers; ++l) {
     const tb_status s = check_layer(ctx, l);
     if (s != TB_OK) return s;
-    tc = tc && ctx->layers[l].kl.page_table == nullptr;
+    tc = tc && ctx->layers[l].kl.page_table == nullptr && !ctx->layers[l].kv8;
   }
   if (count == 0) return TB_OK;
-  if (!tc) {  // fp32 or paged caches: the FMA projection, layer by layer
+  if (!tc) {  // fp32, paged or 8-bit caches: the FMA projection, layer by layer
     for (int l = first_layer; l < first_layer + n_layers; ++l) {
       const tb_status s = tb_project_kimp(ctx, l, start, count, stream);
       if (s != TB_OK) return s;

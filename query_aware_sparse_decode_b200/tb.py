@@ -17,6 +17,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtb.so")
 TB_OK = 0
 TB_BF16, TB_F32 = 0, 1
 TB_BUTLER, TB_SOFTVOTE, TB_BUTLER_GROUP = 0, 1, 2
+TB_KV8_E4M3, TB_KV8_INT8, KV8_BLOCK = 1, 2, 16
 TB_MASK_PER_HEAD, TB_MASK_SHARED, TB_MASK_DENSE, TB_MASK_GROUP = 0, 1, 2, 3
 MAX_BATCH = 128
 MAX_LAYERS = 64
@@ -31,7 +32,8 @@ EXPORTS = ("tb_workspace_size", "tb_init", "tb_bind_layer", "tb_set_seq_lens", "
            "tb_sparse_attn_idx", "tb_decode_step", "tb_select_prefill", "tb_softvote_scores", "tb_sparse_attn_static", "tb_trace_events", "tb_launch_count",
            "tb_check_status", "tb_status_string", "tb_destroy", "tb_selftest_bounded_wait", "tb_selection_cache_size",
            "tb_bind_selection_cache", "tb_set_reuse", "tb_copy_step_masks", "tb_bind_layer_paged", "tb_shard_set",
-           "tb_shard_hist", "tb_shard_pick", "tb_shard_mask", "tb_sparse_attn_partial", "tb_merge_partials")
+           "tb_shard_hist", "tb_shard_pick", "tb_shard_mask", "tb_sparse_attn_partial", "tb_merge_partials",
+           "tb_bind_layer_kv8", "tb_bind_layer_kv8_paged", "tb_append_kv_rows", "tb_read_kv")
 
 
 class TBError(RuntimeError):
@@ -100,6 +102,10 @@ def lib():
             "tb_shard_mask": [vp, i32, vp, vp, vp, vp],
             "tb_sparse_attn_partial": [vp, i32, vp, vp, i32, vp, vp],
             "tb_merge_partials": [vp, vp, i32, vp, vp, vp],
+            "tb_bind_layer_kv8": [vp, i32, i32, vp, vp, vp, vp, vp, vp],
+            "tb_bind_layer_kv8_paged": [vp, i32, i32, vp, vp, vp, vp, i32, vp, i32, i32, vp, vp],
+            "tb_append_kv_rows": [vp, i32, vp, vp, P(ctypes.c_int64), P(ctypes.c_int64), P(ctypes.c_int32), vp],
+            "tb_read_kv": [vp, i32, i32, i32, vp, vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -150,6 +156,21 @@ def kimp_cache(cfg: Config, device="cuda", fill=0.0) -> torch.Tensor:
     (256-token tiles, dimension-major inside), fp32 or bf16 as cfg says."""
     dt = torch.bfloat16 if cfg.kimp_bf16 else torch.float32
     return torch.full((cfg.batch, cfg.n_kv_heads, cfg.max_len // 256, cfg.d_imp, 256), fill, dtype=dt, device=device)
+
+
+KV8_FORMATS = {"e4m3": (TB_KV8_E4M3, torch.float8_e4m3fn), "int8": (TB_KV8_INT8, torch.int8)}
+
+
+def kv8_cache(cfg: Config, fmt: str, device="cuda"):
+    """A zero-filled 8-bit K/V cache for `cfg` ("e4m3" or "int8"): k_codes, v_codes
+    [B][Hkv][max_len][D] and k_scale, v_scale [B][Hkv][max_len/16] (fp32)."""
+    if fmt not in KV8_FORMATS:
+        raise ValueError(f"the 8-bit format must be 'e4m3' or 'int8', not {fmt!r}")
+    rows = (cfg.batch, cfg.n_kv_heads, cfg.max_len)
+    codes = [torch.zeros((*rows, cfg.head_dim), dtype=torch.int8, device=device).view(KV8_FORMATS[fmt][1])
+             for _ in range(2)]
+    scales = [torch.zeros((*rows[:2], cfg.max_len // KV8_BLOCK), dtype=torch.float32, device=device) for _ in range(2)]
+    return codes[0], codes[1], scales[0], scales[1]
 
 
 def workspace_size(cfg: Config) -> int:
@@ -269,6 +290,93 @@ class Context:
         _check(lib().tb_bind_layer_paged(self._h, layer, _ptr(k_pool), _ptr(v_pool), num_pages, _ptr(page_table),
                                          page_size, max_pages, _ptr(kimp_cache), _ptr(w_k)), "tb_bind_layer_paged")
         self._keep[layer] = (k_pool, v_pool, page_table, kimp_cache, w_k)
+
+    # ---- 8-bit K/V caches
+    def _expect(self, name, t, shape, dtype) -> None:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the context on {self.device}")
+
+    def _kv_torch_dtype(self):
+        return torch.bfloat16 if self.cfg.kv_dtype == TB_BF16 else torch.float32
+
+    def _own_stream(self, stream) -> ctypes.c_void_p:
+        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _check_kv8(self, lead, rows, k, v, k_scale, v_scale, kimp_cache, w_k) -> int:
+        c = self.cfg
+        fmt = next((code for code, dt in KV8_FORMATS.values() if dt == k.dtype), None)
+        if fmt is None:
+            raise TypeError(f"8-bit codes must be torch.float8_e4m3fn or torch.int8, got {k.dtype}")
+        for name, t in (("k codes", k), ("v codes", v)):
+            self._expect(name, t, (lead, c.n_kv_heads, rows, c.head_dim), k.dtype)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            self._expect(name, t, (lead, c.n_kv_heads, rows // KV8_BLOCK), torch.float32)
+        self._kimp_type_ok(kimp_cache)
+        self._expect("K_imp cache", kimp_cache, (c.batch, c.n_kv_heads, c.max_len // 256, c.d_imp, 256),
+                     kimp_cache.dtype)
+        self._expect("w_k", w_k, (c.head_dim, c.d_imp), self._kv_torch_dtype())
+        return fmt
+
+    def bind_layer_kv8(self, layer: int, k_codes, v_codes, k_scale, v_scale, kimp_cache, w_k) -> None:
+        """An 8-bit layer (see kv8_cache): the format follows the codes' dtype
+        (torch.float8_e4m3fn or torch.int8)."""
+        fmt = self._check_kv8(self.cfg.batch, self.cfg.max_len, k_codes, v_codes, k_scale, v_scale, kimp_cache, w_k)
+        _check(lib().tb_bind_layer_kv8(self._h, layer, fmt, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
+                                       _ptr(v_scale), _ptr(kimp_cache), _ptr(w_k)), "tb_bind_layer_kv8")
+        self._keep[layer] = (k_codes, v_codes, k_scale, v_scale, kimp_cache, w_k)
+
+    def bind_layer_kv8_paged(self, layer: int, k_pool, v_pool, k_scale, v_scale, page_table, kimp_cache, w_k) -> None:
+        """k_pool, v_pool: [pages][Hkv][page_size][D] codes; k_scale, v_scale:
+        [pages][Hkv][page_size/16]; page_table: [B][max_pages] int32 (device)."""
+        num_pages, _, page_size, _ = k_pool.shape
+        fmt = self._check_kv8(num_pages, page_size, k_pool, v_pool, k_scale, v_scale, kimp_cache, w_k)
+        self._expect("page_table", page_table, (self.cfg.batch, page_table.shape[-1]), torch.int32)
+        _check(lib().tb_bind_layer_kv8_paged(self._h, layer, fmt, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
+                                             _ptr(v_scale), num_pages, _ptr(page_table), page_size,
+                                             page_table.shape[1], _ptr(kimp_cache), _ptr(w_k)),
+               "tb_bind_layer_kv8_paged")
+        self._keep[layer] = (k_pool, v_pool, k_scale, v_scale, page_table, kimp_cache, w_k)
+
+    def append_kv_rows(self, layer: int, k, v, counts=None, stream=None) -> None:
+        """Quantises and appends k[b, :, :counts[b]] and v likewise to every
+        sequence of an 8-bit layer, and forms their K_imp.  k, v:
+        [B][Hkv][n][D] (kv_dtype), any strides with contiguous rows (a view
+        of a fused projection's output serves); counts: n for all by default."""
+        c = self.cfg
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError(f"k and v must be [B][Hkv][n][D] alike, got {tuple(k.shape)} and {tuple(v.shape)}")
+        n = k.shape[2]
+        for name, t in (("k", k), ("v", v)):
+            self._expect(name, t, (c.batch, c.n_kv_heads, n, c.head_dim), self._kv_torch_dtype())
+            if t.stride(3) != 1:
+                raise ValueError(f"{name}: a row's elements must be contiguous")
+        counts = [n] * c.batch if counts is None else [int(x) for x in counts]
+        if len(counts) != c.batch or any(x < 0 or x > n for x in counts):
+            raise ValueError(f"counts must be {c.batch} numbers in [0, {n}], got {counts}")
+        if n == 0:
+            return
+        strides = [(ctypes.c_int64 * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))) for t in (k, v)]
+        with torch.cuda.device(self.device):
+            _check(lib().tb_append_kv_rows(self._h, layer, ctypes.c_void_p(k.data_ptr()),
+                                           ctypes.c_void_p(v.data_ptr()), strides[0], strides[1],
+                                           (ctypes.c_int32 * c.batch)(*counts), self._own_stream(stream)),
+                   "tb_append_kv_rows")
+
+    def read_kv(self, layer: int, start: int, count: int, k_out=None, v_out=None, stream=None) -> None:
+        """Rows [start, start + count) of an 8-bit layer as values into k_out
+        and/or v_out [B][Hkv][count][D] (kv_dtype); rows past a sequence's
+        length are left as they are."""
+        c = self.cfg
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
+                self._expect(name, t, (c.batch, c.n_kv_heads, count, c.head_dim), self._kv_torch_dtype())
+        with torch.cuda.device(self.device):
+            _check(lib().tb_read_kv(self._h, layer, start, count, _ptr(k_out), _ptr(v_out), self._own_stream(stream)),
+                   "tb_read_kv")
 
     def selection_cache(self, layer: int):
         """Allocate (zero-filled) and bind layer `layer`'s selection cache;
