@@ -400,6 +400,14 @@ static tb_status launch_select(tb_ctx* ctx, int layer, const float* scores, bool
 }
 
 // The split attention kernel over an 8-bit layer (the partials' combine is the caller's).
+template <int F, int D, int GS>
+static tb_status launch_attn_kv8_as(bool bf16, const AttnKv8Params& p, dim3 grid, cudaStream_t st) {
+  auto k = bf16 ? attn_kv8_kernel<F, D, GS> : attn_kv8_fma_kernel<float, F, D, GS>;
+  const int smem = bf16 ? attn_kv8_smem<D, GS>() : attn_kv8_fma_smem<D, GS>();
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TB_ERR_CUDA;
+  launch_pdl(k, grid, dim3(kAttnThreads), smem, st, p);
+  return cuda_status(cudaGetLastError());
+}
 static tb_status launch_attn_kv8(const tb_ctx* ctx, const LayerState& ls, const AttnParams& base, dim3 grid,
                                  cudaStream_t st) {
   const tb_config& c = ctx->cfg;
@@ -408,25 +416,15 @@ static tb_status launch_attn_kv8(const tb_ctx* ctx, const LayerState& ls, const 
   static_cast<AttnParams&>(p) = base;
   p.k_scale = ls.k_scale;
   p.v_scale = ls.v_scale;
-#define TB_KV8_CASE(T, F, DV, GSV)                                                                   \
-  if (ls.kv8 == F && c.head_dim == DV && gs == GSV) {                                                \
-    auto k = attn_kv8_fma_kernel<T, F, DV, GSV>;                                                     \
-    const int smem = attn_kv8_fma_smem<DV, GSV>();                                                   \
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)   \
-      return TB_ERR_CUDA;                                                                            \
-    launch_pdl(k, grid, dim3(kAttnThreads), smem, st, p);                                            \
-  } else
-#define TB_KV8_CASES(T, F)                                                                                        \
-  TB_KV8_CASE(T, F, 128, 4) TB_KV8_CASE(T, F, 128, 2) TB_KV8_CASE(T, F, 128, 1) TB_KV8_CASE(T, F, 128, 8)   \
-  TB_KV8_CASE(T, F, 64, 4) TB_KV8_CASE(T, F, 64, 2) TB_KV8_CASE(T, F, 64, 1) TB_KV8_CASE(T, F, 64, 8)
-  if (c.kv_dtype == TB_BF16) {
-    TB_KV8_CASES(__nv_bfloat16, TB_KV8_E4M3) TB_KV8_CASES(__nv_bfloat16, TB_KV8_INT8) return TB_ERR_UNSUPPORTED;
-  } else {
-    TB_KV8_CASES(float, TB_KV8_E4M3) TB_KV8_CASES(float, TB_KV8_INT8) return TB_ERR_UNSUPPORTED;
-  }
+#define TB_KV8_CASE(F, DV, GSV) \
+  if (ls.kv8 == F && c.head_dim == DV && gs == GSV) return launch_attn_kv8_as<F, DV, GSV>(c.kv_dtype == TB_BF16, p, grid, st);
+#define TB_KV8_CASES(F)                                                                           \
+  TB_KV8_CASE(F, 128, 4) TB_KV8_CASE(F, 128, 2) TB_KV8_CASE(F, 128, 1) TB_KV8_CASE(F, 128, 8) \
+  TB_KV8_CASE(F, 64, 4) TB_KV8_CASE(F, 64, 2) TB_KV8_CASE(F, 64, 1) TB_KV8_CASE(F, 64, 8)
+  TB_KV8_CASES(TB_KV8_E4M3) TB_KV8_CASES(TB_KV8_INT8)
 #undef TB_KV8_CASES
 #undef TB_KV8_CASE
-  return cuda_status(cudaGetLastError());
+  return TB_ERR_UNSUPPORTED;
 }
 
 static tb_status launch_attn(tb_ctx* ctx, int layer, const void* q, const uint32_t* mask, int mode, void* out,
