@@ -20,7 +20,7 @@ struct AttnKv8Params : AttnParams {
 
 constexpr int kKv8ListBytes = ((kAttnMaxChunk + kAttnTile) * 5 + 15) / 16 * 16;
 template <int D, int GS>
-constexpr int attn_kv8_fma_smem() { return kKv8ListBytes + kAttnWarps * GS * (D + 2) * 4; }
+constexpr int attn_kv8_f32_smem() { return kKv8ListBytes + kAttnWarps * GS * (D + 2) * 4; }
 
 // The gather list of a sub-chunk, page ids checked: a token whose page is not
 // one of the pool's is listed without a head (nothing reads its codes as a
@@ -39,9 +39,9 @@ __device__ __forceinline__ int build_union_list_kv8(const AttnKv8Params& p, int 
   });
 }
 
-// fp32 FMA: one warp per token at a time, lane owns D/32 consecutive dims.
-template <typename T, int FMT, int D, int GS>
-__global__ void __launch_bounds__(kAttnThreads) attn_kv8_fma_kernel(const AttnKv8Params p) {
+// fp32 queries, fp32 FMA: one warp per token at a time, lane owns D/32 consecutive dims.
+template <int FMT, int D, int GS>
+__global__ void __launch_bounds__(kAttnThreads) attn_kv8_f32_kernel(const AttnKv8Params p) {
   pdl_wait();
   pdl_trigger();
   constexpr int DPL = D / 32;
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kv8_fma_kernel(const AttnKv
     l[hh] = 0.f;
 #pragma unroll
     for (int j = 0; j < DPL; ++j) {
-      q[hh][j] = to_f32(reinterpret_cast<const T*>(p.q)[((size_t)b * p.Hq + g * GS + hh) * D + lane * DPL + j]);
+      q[hh][j] = reinterpret_cast<const float*>(p.q)[((size_t)b * p.Hq + g * GS + hh) * D + lane * DPL + j];
       o[hh][j] = 0.f;
     }
   }

@@ -39,6 +39,7 @@ __device__ __forceinline__ int kv8_exponent(float amax) {
   const int e = FMT == kFmtE4m3 ? ex - 8 + (mant > 0x600000u) : ex - 6 + (mant > 0x7E0000u);
   return e < kKv8MinExp ? kKv8MinExp : e;
 }
+// 2^e, -126 <= e <= 127
 __device__ __forceinline__ float kv8_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // magnitude that counts towards amax: infinities and NaN do not
@@ -110,14 +111,15 @@ struct Kv8WriteParams {
   int cnt[kMaxBatch];        // rows written
 };
 
-// One CTA per touched block of 16 tokens of a (b, g): grid (blocks, Hkv, B),
-// 128 threads.  Both tensors' new rows are staged in shared memory as fp32; the
+// fp32 rows: one CTA per touched block of 16 tokens of a (b, g): grid (blocks,
+// Hkv, B), 128 threads.  Both tensors' new rows are staged in shared memory as fp32; the
 // block's amax gives the scale; rows of the block that were cached before are
 // re-rounded when the scale grows.  Rows behind the last written one keep their
 // codes.  K_imp of the new rows comes from the unrounded values.
 constexpr int kKv8WriteThreads = 128;
-template <typename T, int FMT, int D>
-__global__ void __launch_bounds__(kKv8WriteThreads) kv8_write_kernel(const Kv8WriteParams p) {
+template <int FMT, int D>
+__global__ void __launch_bounds__(kKv8WriteThreads) kv8_write_f32_kernel(const Kv8WriteParams p) {
+  using T = float;
   pdl_wait();
   pdl_trigger();
   constexpr int NT = kKv8WriteThreads;
@@ -185,6 +187,196 @@ __global__ void __launch_bounds__(kKv8WriteThreads) kv8_write_kernel(const Kv8Wr
   }
 }
 
+// bf16 rows: one warp per touched block, everything in registers.  Lane (grp,
+// tq) loads 16-byte pieces (dims 32i + 8tq ..) of rows grp and grp + 8 of K and
+// of V: 16 rows of both are in flight at once.  The same registers are the A
+// fragments of K_imp = K W_K on mma.sync m16n8k16 (the k indices of step
+// 2i + h are dims 32i + 8tq + 4h + {0,1 | 2,3}), the input of the block's amax
+// (one warp maximum) and of the codes, stored 8 bytes a lane in whole
+// 32-byte sectors.  W_K's B fragments are staged once per CTA, in lane order.
+// A warp's blocks are gridDim.x apart, so few blocks spread over the CTAs.
+struct Kv8WriteBf16Params : Kv8WriteParams {
+  int first[kMaxBatch + 1];  // units (block, head) before sequence b's; [B]: all of them
+  int batch;
+};
+
+// largest |x| pattern of a bf16 pair; NaN patterns exceed infinity's
+__device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t m, uint32_t w) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w & 0x7FFF7FFFu));
+  return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// codes of x0..x3 (finite, |x| inv <= F) in a word
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_encode4(float x0, float x1, float x2, float x3, float inv) {
+  if constexpr (FMT == kFmtE4m3) {
+    uint16_t a, c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x1 * inv), "f"(x0 * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x3 * inv), "f"(x2 * inv));
+    return (uint32_t)a | (uint32_t)c << 16;
+  } else {
+    // adding 1.5 * 2^23 rounds to an integer (ties to even) in the low mantissa bits
+    const float magic = 12582912.f;
+    const uint32_t a = __byte_perm(__float_as_uint(fmaf(x0, inv, magic)), __float_as_uint(fmaf(x1, inv, magic)), 0x0040);
+    const uint32_t c = __byte_perm(__float_as_uint(fmaf(x2, inv, magic)), __float_as_uint(fmaf(x3, inv, magic)), 0x0040);
+    return __byte_perm(a, c, 0x5410);
+  }
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_encode4_any(float x0, float x1, float x2, float x3, float inv) {
+  return (uint32_t)kv8_encode<FMT>(x0 * inv) | (uint32_t)kv8_encode<FMT>(x1 * inv) << 8 |
+         (uint32_t)kv8_encode<FMT>(x2 * inv) << 16 | (uint32_t)kv8_encode<FMT>(x3 * inv) << 24;
+}
+
+template <int FMT, int D, int DIMP>
+__global__ void __launch_bounds__(kKv8WriteThreads, 4) kv8_write_bf16_kernel(const Kv8WriteBf16Params p) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int KST = D / 16, NT = DIMP / 8, NP = D / 32;
+  __shared__ uint2 wf[KST * NT * 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int grp = lane >> 2, tq = lane & 3;
+  {
+    const uint16_t* W = reinterpret_cast<const uint16_t*>(p.w_k);
+#pragma unroll
+    for (int e = tid; e < KST * NT * 32; e += kKv8WriteThreads) {
+      const int ln = e & 31, nt = (e >> 5) % NT, kk = (e >> 5) / NT;
+      const uint16_t* w = W + (32 * (kk >> 1) + 8 * (ln & 3) + 4 * (kk & 1)) * DIMP + 8 * nt + (ln >> 2);
+      wf[e] = make_uint2((uint32_t)w[0] | (uint32_t)w[DIMP] << 16, (uint32_t)w[2 * DIMP] | (uint32_t)w[3 * DIMP] << 16);
+    }
+  }
+  __syncthreads();
+  const int units = p.first[p.batch];
+  for (int u = blockIdx.x + warp * gridDim.x; u < units; u += gridDim.x * (kKv8WriteThreads / 32)) {
+    int b = 0;
+    for (int hi = p.batch; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (p.first[mid] <= u) b = mid;
+      else hi = mid;
+    }
+    const int pos = p.pos[b], end = pos + p.cnt[b];
+    const int per_head = (p.first[b + 1] - p.first[b]) / p.Hkv;
+    const int g = (u - p.first[b]) / per_head;
+    const int t_lo = (pos / kKv8Block + (u - p.first[b]) % per_head) * kKv8Block;
+    const int r0 = max(pos - t_lo, 0), r1 = min(end - t_lo, kKv8Block);
+    uint32_t row0;
+    if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t_lo, &row0)) {
+      if (lane == 0) atomicOr(p.status, TB_DEV_ERR_INDEX);
+      continue;
+    }
+    uint4 x[2][2][NP];  // [K, V][row grp, row grp + 8][piece]
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(p.src[kv]) + b * p.sb[kv] + g * p.sh[kv] +
+                            (long long)(t_lo - pos) * p.st[kv] + 8 * tq;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = grp + 8 * h;
+        const bool fresh = r >= r0 && r < r1;
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          x[kv][h][i] = fresh ? __ldcs(reinterpret_cast<const uint4*>(src + r * p.st[kv] + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const uint4 w = x[kv][h][i];
+          m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, w.x), w.y), w.z), w.w);
+        }
+      uint32_t top = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+      const bool odd = top >= 0x7F80u;  // an infinity or a NaN
+      if (odd) {
+        float a = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const uint32_t w[4] = {x[kv][h][i].x, x[kv][h][i].y, x[kv][h][i].z, x[kv][h][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a = fmaxf(a, fmaxf(kv8_mag(bf16_lo(w[j])), kv8_mag(bf16_hi(w[j]))));
+          }
+        top = __reduce_max_sync(0xffffffffu, __float_as_uint(a) >> 16);
+        if (lane == 0) atomicOr(p.status, TB_DEV_ERR_VALUE);
+      }
+      float sc = kv8_pow2(kv8_exponent<FMT>(__uint_as_float(top << 16)));
+      float ratio = 1.f;  // of the old scale to the new one, for the block's older rows
+      if (r0 > 0) {
+        const float old = p.scale[kv][row0 >> 4];
+        if (old >= sc) sc = old;
+        else ratio = old * (1.f / sc);
+      }
+      const float inv = 1.f / sc;
+      uint8_t* dst = p.codes[kv] + (size_t)row0 * D + 8 * tq;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = grp + 8 * h;
+        if (r >= r0 && r < r1) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const uint4 w = x[kv][h][i];
+            uint2 c;
+            if (!odd) {
+              c.x = kv8_encode4<FMT>(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), inv);
+              c.y = kv8_encode4<FMT>(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w), inv);
+            } else {
+              c.x = kv8_encode4_any<FMT>(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), inv);
+              c.y = kv8_encode4_any<FMT>(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w), inv);
+            }
+            *reinterpret_cast<uint2*>(dst + r * D + 32 * i) = c;
+          }
+        } else if (r < r0 && ratio != 1.f) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            uint2* at = reinterpret_cast<uint2*>(dst + r * D + 32 * i);
+            float y[4], z[4];
+            kv8_decode4<FMT>(at->x, y);
+            kv8_decode4<FMT>(at->y, z);
+            *at = make_uint2(kv8_encode4_any<FMT>(y[0], y[1], y[2], y[3], ratio),
+                             kv8_encode4_any<FMT>(z[0], z[1], z[2], z[3], ratio));
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the old scale
+      if (lane == 0) p.scale[kv][row0 >> 4] = sc;
+      if (kv == 0) {
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const uint4 w0 = x[0][0][i], w1 = x[0][1][i];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 f0 = wf[(2 * i * NT + nt) * 32 + lane], f1 = wf[((2 * i + 1) * NT + nt) * 32 + lane];
+            mma_16816(acc[nt], w0.x, w1.x, w0.y, w1.y, f0.x, f0.y);
+            mma_16816(acc[nt], w0.z, w1.z, w0.w, w1.w, f1.x, f1.y);
+          }
+        }
+        const size_t slab = (size_t)b * p.Hkv + g;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = grp + 8 * h;
+          if (r < r0 || r >= r1) continue;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              store_kimp(p.kimp, kimp_index(slab, 8 * nt + 2 * tq + e, t_lo + r, DIMP, p.max_len), acc[nt][2 * h + e],
+                         p.kimp_bf16);
+        }
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------ reading rows
 struct Kv8ReadParams {
   const uint8_t* codes[2];
@@ -197,37 +389,62 @@ struct Kv8ReadParams {
 };
 
 // out[b][g][t - start] = code * scale for t < len[b]; rows past the length are
-// left alone.  A thread decodes 16 codes (one 16-byte load); grid
-// (ceil(count * D/16 / 256), Hkv, B).
+// left alone.  A thread turns codes into 16 bytes of output, kKv8ReadPieces
+// times, so that loads and stores of a warp are contiguous and several are
+// in flight; grid (ceil(count * pieces / (256 kKv8ReadPieces)), Hkv, B).
+constexpr int kKv8ReadPieces = 4;
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const Kv8ReadParams p) {
   pdl_wait();
   pdl_trigger();
-  constexpr int NP = D / 16;
+  constexpr int CW = 4 / sizeof(T);   // words of codes per piece: 2 (bf16) or 1 (fp32)
+  constexpr int NP = D / (4 * CW);    // pieces per row
   const int g = blockIdx.y, b = blockIdx.z;
-  const int e = blockIdx.x * 256 + threadIdx.x;
-  const int i = e / NP, part = e % NP, t = p.start + i;
-  if (i >= p.count || t >= p.lens[b]) return;
-  uint32_t row;
-  if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &row)) {
-    atomicOr(p.status, TB_DEV_ERR_INDEX);
-    return;
+  const int n = min(p.count, p.lens[b] - p.start);
+  const long long e0 = (long long)blockIdx.x * (256 * kKv8ReadPieces) + threadIdx.x;
+  uint32_t c[2][kKv8ReadPieces][CW];
+  float s[2][kKv8ReadPieces];
+#pragma unroll
+  for (int u = 0; u < kKv8ReadPieces; ++u) {
+    const int i = (int)((e0 + u * 256) / NP), part = (int)((e0 + u * 256) % NP);
+    uint32_t row = 0;
+    bool ok = i < n;
+    if (ok && !kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, p.start + i, &row)) {
+      atomicOr(p.status, TB_DEV_ERR_INDEX);
+      ok = false;
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      s[kv][u] = -1.f;  // nothing to write
+      if (!ok || p.out[kv] == nullptr) continue;
+      s[kv][u] = p.scale[kv][row >> 4];
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.codes[kv] + (size_t)row * D) + part * CW;
+      if constexpr (CW == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(src);
+        c[kv][u][0] = w.x;
+        c[kv][u][1] = w.y;
+      } else {
+        c[kv][u][0] = *src;
+      }
+    }
   }
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    if (p.out[kv] == nullptr) continue;
-    const uint4 c = *reinterpret_cast<const uint4*>(p.codes[kv] + (size_t)row * D + part * 16);
-    const float s = p.scale[kv][row >> 4];
-    T* out = reinterpret_cast<T*>(p.out[kv]) + (((size_t)b * p.Hkv + g) * p.count + i) * D + part * 16;
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  for (int u = 0; u < kKv8ReadPieces; ++u) {
+    const long long e = e0 + u * 256;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float x[4];
-      kv8_decode4<FMT>(w[q], x);
-      if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint2*>(out + 4 * q) = make_uint2(pack_bf16(x[0] * s, x[1] * s), pack_bf16(x[2] * s, x[3] * s));
+    for (int kv = 0; kv < 2; ++kv) {
+      const float f = s[kv][u];
+      if (f < 0.f) continue;
+      uint8_t* out = reinterpret_cast<uint8_t*>(p.out[kv]) +
+                     (((size_t)b * p.Hkv + g) * p.count * NP + (size_t)e) * 16;
+      float x[4], y[4];
+      kv8_decode4<FMT>(c[kv][u][0], x);
+      if constexpr (CW == 2) {
+        kv8_decode4<FMT>(c[kv][u][CW - 1], y);
+        *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f),
+                                                    pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f));
       } else {
-        *reinterpret_cast<float4*>(out + 4 * q) = make_float4(x[0] * s, x[1] * s, x[2] * s, x[3] * s);
+        *reinterpret_cast<float4*>(out) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
       }
     }
   }

@@ -402,8 +402,8 @@ static tb_status launch_select(tb_ctx* ctx, int layer, const float* scores, bool
 // The split attention kernel over an 8-bit layer (the partials' combine is the caller's).
 template <int F, int D, int GS>
 static tb_status launch_attn_kv8_as(bool bf16, const AttnKv8Params& p, dim3 grid, cudaStream_t st) {
-  auto k = bf16 ? attn_kv8_kernel<F, D, GS> : attn_kv8_fma_kernel<float, F, D, GS>;
-  const int smem = bf16 ? attn_kv8_smem<D, GS>() : attn_kv8_fma_smem<D, GS>();
+  auto k = bf16 ? attn_kv8_kernel<F, D, GS> : attn_kv8_f32_kernel<F, D, GS>;
+  const int smem = bf16 ? attn_kv8_smem<D, GS>() : attn_kv8_f32_smem<D, GS>();
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TB_ERR_CUDA;
   launch_pdl(k, grid, dim3(kAttnThreads), smem, st, p);
   return cuda_status(cudaGetLastError());
@@ -847,7 +847,7 @@ static tb_status launch_kv8_write(tb_ctx* ctx, int layer, const void* k, const v
                                   const int64_t* vs, const int32_t* cnt, cudaStream_t st) {
   const tb_config& c = ctx->cfg;
   LayerState& ls = ctx->layers[layer];
-  Kv8WriteParams p{};
+  Kv8WriteBf16Params p{};
   p.src[0] = k;
   p.src[1] = v;
   for (int i = 0; i < 2; ++i) {
@@ -869,29 +869,35 @@ static tb_status launch_kv8_write(tb_ctx* ctx, int layer, const void* k, const v
   p.max_len = c.max_len;
   p.kimp_bf16 = c.kimp_bf16;
   int blocks = 0;  // most blocks that one sequence's new rows touch
+  long long units = 0;
   for (int b = 0; b < c.batch; ++b) {
     if (cnt[b] < 0) return TB_ERR_INVALID_ARG;
     if ((long long)ls.lens[b] + cnt[b] > c.max_len) return TB_ERR_CAPACITY;
     p.pos[b] = ls.lens[b];
     p.cnt[b] = cnt[b];
-    if (cnt[b] > 0)
-      blocks = std::max(blocks, (ls.lens[b] % kKv8Block + cnt[b] + kKv8Block - 1) / kKv8Block);
+    const int nb = cnt[b] > 0 ? (ls.lens[b] % kKv8Block + cnt[b] + kKv8Block - 1) / kKv8Block : 0;
+    blocks = std::max(blocks, nb);
+    p.first[b] = (int)units;
+    units += (long long)nb * c.n_kv_heads;  // B * Hkv * max_len < 2^31
   }
+  p.first[c.batch] = (int)units;
+  p.batch = c.batch;
   if (blocks == 0) return TB_OK;
-  const dim3 grid((unsigned)blocks, c.n_kv_heads, c.batch);
-#define TB_KV8_WRITE(T, F, DV)                                                      \
-  if (ls.kv8 == F && c.head_dim == DV)                                              \
-    launch_pdl(kv8_write_kernel<T, F, DV>, grid, dim3(kKv8WriteThreads), 0, st, p); \
-  else
-#define TB_KV8_WRITES(T)                                                                                   \
-  TB_KV8_WRITE(T, TB_KV8_E4M3, 128) TB_KV8_WRITE(T, TB_KV8_E4M3, 64) TB_KV8_WRITE(T, TB_KV8_INT8, 128) \
-  TB_KV8_WRITE(T, TB_KV8_INT8, 64) return TB_ERR_UNSUPPORTED;
-  if (c.kv_dtype == TB_BF16) {
-    TB_KV8_WRITES(__nv_bfloat16)
-  } else {
-    TB_KV8_WRITES(float)
-  }
-#undef TB_KV8_WRITES
+  // bf16: at most four CTAs per SM, so that a long write stages W_K a few hundred times
+  const dim3 grid_bf16((unsigned)std::min<long long>(units, 4LL * ctx->num_sms));
+  const dim3 grid_f32((unsigned)blocks, c.n_kv_heads, c.batch);
+  const Kv8WriteParams& pf = p;
+#define TB_KV8_WRITE(F, DV)                                                                                      \
+  if (ls.kv8 == F && c.head_dim == DV) {                                                                         \
+    if (c.kv_dtype == TB_F32)                                                                                    \
+      launch_pdl(kv8_write_f32_kernel<F, DV>, grid_f32, dim3(kKv8WriteThreads), 0, st, pf);                      \
+    else if (c.d_imp == 32)                                                                                      \
+      launch_pdl(kv8_write_bf16_kernel<F, DV, 32>, grid_bf16, dim3(kKv8WriteThreads), 0, st, p);                 \
+    else                                                                                                         \
+      launch_pdl(kv8_write_bf16_kernel<F, DV, 16>, grid_bf16, dim3(kKv8WriteThreads), 0, st, p);                 \
+  } else
+  TB_KV8_WRITE(TB_KV8_E4M3, 128) TB_KV8_WRITE(TB_KV8_E4M3, 64) TB_KV8_WRITE(TB_KV8_INT8, 128)
+  TB_KV8_WRITE(TB_KV8_INT8, 64) return TB_ERR_UNSUPPORTED;
 #undef TB_KV8_WRITE
   ++ctx->launches;
   const tb_status s = cuda_status(cudaGetLastError());
@@ -946,7 +952,9 @@ TB_API tb_status tb_read_kv(tb_ctx* ctx, int layer, int start, int count, void* 
   for (int b = 0; b < c.batch; ++b) p.lens[b] = ls.lens[b];
   const int n = std::min(count, max_len_of(ls, c.batch) - start);  // rows that some sequence holds
   if (n <= 0) return TB_OK;
-  const dim3 grid((unsigned)(((long long)n * (c.head_dim / 16) + 255) / 256), c.n_kv_heads, c.batch);
+  const int pieces = c.head_dim / (c.kv_dtype == TB_BF16 ? 8 : 4);  // 16 bytes of output each
+  const long long per_cta = 256 * kKv8ReadPieces;
+  const dim3 grid((unsigned)(((long long)n * pieces + per_cta - 1) / per_cta), c.n_kv_heads, c.batch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 #define TB_KV8_READ(T, F, DV)                                         \
   if (ls.kv8 == F && c.head_dim == DV)                                \
