@@ -18,6 +18,41 @@ struct AttnKv8Params : AttnParams {
   const float* v_scale;
 };
 
+// Split of the 8-bit attention (host side): the shortest chunks (whole mask
+// words) that keep all of the call's CTAs in one wave of kKv8CtasPerSm per SM,
+// counting the tokens that each sequence has.
+constexpr int kKv8CtasPerSm = 4;
+constexpr int kKv8MinChunk = 128;
+inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch, int max_splits, int* chunk_out,
+                           int* nsplit_out) {
+  long long total = 0;
+  int longest = 1;
+  for (int b = 0; b < batch; ++b) {
+    total += lens[b];
+    longest = lens[b] > longest ? lens[b] : longest;
+  }
+  const long long slots = (long long)kKv8CtasPerSm * num_sms;
+  long long chunk = (total * kv_heads + slots - 1) / slots;
+  const long long least = (longest + max_splits - 1) / max_splits;
+  chunk = chunk < least ? least : chunk;
+  chunk = chunk < kKv8MinChunk ? kKv8MinChunk : (chunk + 31) / 32 * 32;
+  for (;;) {
+    long long n = 0, next = longest + 31;  // the CTAs, and the next chunk that has fewer
+    for (int b = 0; b < batch; ++b) {
+      const long long ns = (lens[b] + chunk - 1) / chunk;
+      n += ns;
+      if (ns > 1) {
+        const long long c = ((lens[b] + ns - 2) / (ns - 1) + 31) / 32 * 32;
+        next = c < next ? c : next;
+      }
+    }
+    if (n * kv_heads <= slots || chunk >= longest) break;
+    chunk = next > chunk ? next : chunk + 32;
+  }
+  *chunk_out = (int)chunk;
+  *nsplit_out = (int)((longest + chunk - 1) / chunk);
+}
+
 constexpr int kKv8ListBytes = ((kAttnMaxChunk + kAttnTile) * 5 + 15) / 16 * 16;
 template <int D, int GS>
 constexpr int attn_kv8_f32_smem() { return kKv8ListBytes + kAttnWarps * GS * (D + 2) * 4; }
@@ -28,7 +63,7 @@ constexpr int attn_kv8_f32_smem() { return kKv8ListBytes + kAttnWarps * GS * (D 
 template <int GS>
 __device__ __forceinline__ int build_union_list_kv8(const AttnKv8Params& p, int b, int g, int t0, int t1,
                                                     int32_t* list_idx, uint8_t* list_hb, uint32_t* scan_sm) {
-  return build_union<GS>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
+  return build_union<GS, kAttnMaxChunk, kAttnTile>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
     uint32_t row;
     if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &row)) {
       atomicOr(p.status, TB_DEV_ERR_INDEX);
@@ -196,24 +231,63 @@ __device__ __forceinline__ void load_q_f16(const void* q, size_t head0, int grp,
   qs[1] = kv8_pow2(-__shfl_sync(0xffffffffu, up, (8 * tq + 4) & 31));
 }
 
-template <int D, int GS>
+// Ring of one warp: kKv8Stages stages of 32 tokens.
+constexpr int kKv8Stages = 3;
+constexpr int kKv8Tok = 16;       // tokens of an iteration
+constexpr int kKv8MaxList = 1024; // tokens per gather list
+template <int D>
+constexpr int kv8_stage_bytes() { return 2 * kKv8Tok * D; }
+template <int D, int GS, bool DENSE>
 constexpr int attn_kv8_smem() {
-  constexpr int list = (kAttnMaxChunk + kAttnTile) * 6 + (kAttnMaxChunk / kKv8Block) * 8;
+  constexpr int ring = kAttnWarps * kKv8Stages * (kv8_stage_bytes<D>() + (DENSE ? kKv8Tok / 2 : 0));
+  constexpr int list = DENSE ? 0 : (kKv8MaxList + kKv8Tok) * 6 + (kKv8MaxList / kKv8Block) * 8;
   constexpr int merge = kAttnWarps * GS * (D + 2) * 4;
-  return list > merge ? list : merge;
+  return ring + list > merge ? ring + list : merge;
+}
+// 16-byte pieces of a cached row are stored at piece ^ swizzle(row), so that the
+// lanes of a shared-memory phase touch different banks: for K two rows' pieces
+// tq, for V rows 0, 2, 4, 6 (+ 1) of two neighbouring pieces.
+template <int D>
+__device__ __forceinline__ int kv8_swizzle_k(int row) { return D == 128 ? (row & 1) << 2 : 0; }
+template <int D>
+__device__ __forceinline__ int kv8_swizzle_v(int row) { return D == 128 ? row & 6 : (row >> 1) & 3; }
+__device__ __forceinline__ void cp_async_4(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_16u(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
 }
 
 // bf16 queries over 8-bit codes.  As in attn_bf16_kernel a warp takes 16
-// listed tokens at a time as the M rows of S^T = K Q^T and the K dimension of
+// tokens at a time as the M rows of S^T = K Q^T and the K dimension of
 // O^T = V^T P^T, on mma.sync m16n8k16 with fp16 operands (both formats' codes
-// are exact in fp16) and fp32 accumulators.  The codes go from global memory
-// straight into the registers of the A fragments:
-//  - K: lane (grp, tq) loads 16-byte pieces of rows grp and grp + 8; a word
-//    (4 dims) is one k-step's share of a lane, so no shuffle or shared memory;
-//  - V: it loads D/8 bytes (dims grp D/8 ..) of token rows 2tq, 2tq+1, 2tq+8,
+// are exact in fp16) and fp32 accumulators.  The codes reach the A fragments
+// without ldmatrix or shuffles:
+//  - K: lane (grp, tq) takes 16-byte pieces of rows grp and grp + 8; a word
+//    (4 dims) is one k-step's share of a lane;
+//  - V: it takes D/8 bytes (dims grp D/8 ..) of token rows 2tq, 2tq+1, 2tq+8,
 //    2tq+9; byte permutes pair the tokens of a dim, and m-tile mt takes dims
 //    grp D/8 + 2mt and + 2mt + 1 as its rows grp and grp + 8.
-// The next tile's K is requested when S is done, its V when O is done.
+// Two tiles an iteration: their products and conversions are independent, which
+// a warp needs more than bytes in flight (one tile at a time was a chain of about
+// 2100 cycles).  A ring of kKv8Stages iterations per warp holds the loads.  Rows
+// are copied whole (eight lanes a 128-byte row: four lanes that took a sector each of
+// four rows made L2 send half as much again).
+//
+// DENSE takes every token of the chunk: tiles are blocks of the cache, so one
+// row lookup and one scale pair serve a tile and there is no gather list.
+// Otherwise the union of the group's masks is listed as in attn_bf16_kernel,
+// with each token's block in the sub-chunk beside its head bits.
 //
 // Softmax (log2 domain, fp32): l sums p = 2^(x - m); the weights of the V
 // codes are w = 2^(x + log2 vs - r + 7) with their own running exponent r, so
@@ -222,19 +296,21 @@ constexpr int attn_kv8_smem() {
 // 8 (p <= 2^8, w <= 2^15), which after the first tiles is rare, and saves the
 // cross-lane maximum of every tile.  Weights keep fp16's 11 bits down to
 // 2^-21 of the largest one.
-template <int FMT, int D, int GS>
-__global__ void __launch_bounds__(kAttnThreads, 4) attn_kv8_kernel(const AttnKv8Params p) {
+template <int FMT, int D, int GS, bool DENSE>
+__global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(const AttnKv8Params p) {
   pdl_wait();
   pdl_trigger();
   static_assert(D == 64 || D == 128, "head dim");
   constexpr int KSTEPS = D / 16, MT = D / 16;
-  constexpr int KLD = D / 64;  // 16-byte loads of a K row per lane
-  constexpr int VW = D / 32;   // words of a V row per lane
+  constexpr int KLD = D / 64;                   // 16-byte pieces of a K row per lane
+  constexpr int VW = D / 32, VB = D / 8;        // words and bytes of a V row per lane
+  constexpr int U = kKv8Tok / 16;               // mma tiles of an iteration
+  constexpr int VOFF = kKv8Tok * D;             // V slots of a stage
+  constexpr int STAGE = kv8_stage_bytes<D>();
   extern __shared__ __align__(128) uint8_t smem[];
-  int32_t* list_idx = reinterpret_cast<int32_t*>(smem);
-  float2* tab = reinterpret_cast<float2*>(list_idx + kAttnMaxChunk + kAttnTile);  // per block: ks log2e/sqrt(D), log2 vs
-  uint16_t* list_hb = reinterpret_cast<uint16_t*>(tab + kAttnMaxChunk / kKv8Block);
-  __shared__ uint32_t scan_sm[32];
+  int32_t* list_idx = reinterpret_cast<int32_t*>(smem + kAttnWarps * kKv8Stages * STAGE);
+  float2* tab = reinterpret_cast<float2*>(list_idx + kKv8MaxList + kKv8Tok);  // per block: ks log2e/sqrt(D), log2 vs
+  uint16_t* list_hb = reinterpret_cast<uint16_t*>(tab + kKv8MaxList / kKv8Block);
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int L = p.lens[b];
   const int t0 = split * p.chunk;
@@ -242,100 +318,157 @@ __global__ void __launch_bounds__(kAttnThreads, 4) attn_kv8_kernel(const AttnKv8
   const int t1 = min(t0 + p.chunk, L);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = lane >> 2, tq = lane & 3;
-  const uint8_t* Kb = reinterpret_cast<const uint8_t*>(p.k_cache) + 16 * tq;
-  const uint8_t* Vb = reinterpret_cast<const uint8_t*>(p.v_cache) + grp * (D / 8);
+  // copies: whole rows, NPC 16-byte pieces each, CR rows per request; reads: K
+  // pieces tq + 4i of rows grp and grp + 8, V bytes grp VB .. of rows 2tq, + 1, + 8, + 9
+  constexpr int NPC = D / 16, CR = 32 / NPC;
+  const int c_row = lane / NPC, c_part = lane % NPC;
+  const uint8_t* Kb = reinterpret_cast<const uint8_t*>(p.k_cache) + 16 * c_part;
+  const uint8_t* Vb = reinterpret_cast<const uint8_t*>(p.v_cache) + 16 * c_part;
+  const uint32_t ring = smem_u32(smem) + warp * kKv8Stages * STAGE;
+  const uint32_t c_dst = ring + c_row * D, k_src = ring + grp * D, v_src = ring + VOFF + 2 * tq * D + grp * VB % 16;
+  // DENSE: per stage, the (ks, vs) pairs of its two blocks
+  const uint32_t scales = smem_u32(smem) + kAttnWarps * kKv8Stages * STAGE + warp * kKv8Stages * 8 * U;
 
   uint32_t qb[KSTEPS][2];
   float qs[2];
-  load_q_f16<D, GS>(p.q, (size_t)b * p.Hq + g * GS, grp, tq, qb, qs);
   const uint32_t head_bits = ((1u << GS) - 1u) >> (2 * tq) & 3u;
-
   float o[MT][4];  // dims grp D/8 + 2mt (+1), heads 2tq + {0,1}
 #pragma unroll
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   float m_run[2] = {kNegInf, kNegInf}, r_run[2] = {kNegInf, kNegInf}, l_run[2] = {0.f, 0.f};
 
-  for (int sc0 = t0; sc0 < t1; sc0 += kAttnMaxChunk) {
-    const int sc1 = min(sc0 + kAttnMaxChunk, t1);
-    {  // the sub-chunk's block scales: at most one block per thread
+  for (int sc0 = t0, sc1; sc0 < t1; sc0 = sc1) {
+    sc1 = DENSE ? t1 : min(sc0 + kKv8MaxList, t1);  // one gather list each
+    int n = sc1 - sc0;
+    if constexpr (!DENSE) {
+      __shared__ uint32_t scan_sm[32];
+      // the sub-chunk's block scales: at most one block per thread
       const int t = sc0 + tid * kKv8Block;
       uint32_t row;
       if (t < sc1 && kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &row))
         tab[tid] = make_float2(p.k_scale[row >> 4] * p.scale_log2, __log2f(p.v_scale[row >> 4]));
+      n = build_union<GS, kKv8MaxList, kKv8Tok>(p, b, g, sc0, sc1, scan_sm, [&](int pos, int tt, uint32_t hb) {
+        uint32_t rr;
+        if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, tt, &rr)) {
+          atomicOr(p.status, TB_DEV_ERR_INDEX);
+          hb = 0u;
+        }
+        list_idx[pos] = (int32_t)rr;
+        list_hb[pos] = (uint16_t)(hb | (uint32_t)(tt - sc0) / kKv8Block << 8);
+      });
     }
-    const int n = build_union<GS>(p, b, g, sc0, sc1, scan_sm, [&](int pos, int t, uint32_t hb) {
-      uint32_t row;
-      if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &row)) {
-        atomicOr(p.status, TB_DEV_ERR_INDEX);
-        hb = 0u;
-      }
-      list_idx[pos] = (int32_t)row;
-      list_hb[pos] = (uint16_t)(hb | (uint32_t)(t - sc0) / kKv8Block << 8);
-    });
-    const int ntiles = (n + kAttnTile - 1) / kAttnTile;
-    uint4 kc[2][KLD];
-    uint32_t vc[4][VW];
-    auto load_k = [&](int tile) {
+    const int niter = (n + kKv8Tok - 1) / kKv8Tok;
+    const int my_n = niter > warp ? (niter - warp + kAttnWarps - 1) / kAttnWarps : 0;
+    auto issue = [&](int it) {
+      const int base = (warp + it * kAttnWarps) * kKv8Tok;
+      const uint32_t off = (uint32_t)(it % kKv8Stages) * STAGE;
+      uint32_t rows[kKv8Tok / CR];
+      if constexpr (DENSE) {
+        uint32_t row[U];
+        int last[U];  // rows past the end repeat the last one
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint8_t* src = Kb + (size_t)(uint32_t)list_idx[tile * kAttnTile + grp + 8 * r] * D;
-#pragma unroll
-        for (int i = 0; i < KLD; ++i) kc[r][i] = ld_codes16(src + 64 * i);
-      }
-    };
-    auto load_v = [&](int tile) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int2 rows = *reinterpret_cast<const int2*>(list_idx + tile * kAttnTile + 2 * tq + 8 * r);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint8_t* src = Vb + (size_t)(uint32_t)(e ? rows.y : rows.x) * D;
-          if constexpr (VW == 4) {
-            const uint4 v = ld_codes16(src);
-            vc[2 * r + e][0] = v.x;
-            vc[2 * r + e][1] = v.y;
-            vc[2 * r + e][2] = v.z;
-            vc[2 * r + e][3] = v.w;
-          } else {
-            const uint2 v = ld_codes8(src);
-            vc[2 * r + e][0] = v.x;
-            vc[2 * r + e][1] = v.y;
+        for (int u = 0; u < U; ++u) {
+          const int tt = sc0 + base + 16 * u;
+          const bool in = tt < sc1;
+          const bool ok = kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, in ? tt : sc0 + base, &row[u]);
+          last[u] = ok && in ? sc1 - 1 - tt : 0;
+          const uint32_t dst = scales + (it % kKv8Stages) * 8 * U + 8 * u;
+          if (ok) {
+            if (lane == 0) cp_async_4(dst, p.k_scale + (row[u] >> 4));
+            if (lane == 1) cp_async_4(dst + 4, p.v_scale + (row[u] >> 4));
+          } else if (lane == 0) {  // a page outside the pool: the block's scale is NaN
+            atomicOr(p.status, TB_DEV_ERR_INDEX);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(0x7fffffff) : "memory");
           }
         }
+#pragma unroll
+        for (int r = 0; r < kKv8Tok / CR; ++r) {
+          const int u = r * CR / 16;
+          rows[r] = row[u] + min(c_row + CR * r - 16 * u, last[u]);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < kKv8Tok / CR; ++r) rows[r] = (uint32_t)list_idx[base + c_row + CR * r];
+      }
+#pragma unroll
+      for (int r = 0; r < kKv8Tok / CR; ++r) {
+        const size_t src = (size_t)rows[r] * D;
+        const uint32_t dst = c_dst + off + r * CR * D;
+        cp_async_16u(dst + ((c_part ^ kv8_swizzle_k<D>(c_row + CR * r)) << 4), Kb + src);
+        cp_async_16u(dst + VOFF + ((c_part ^ kv8_swizzle_v<D>(c_row + CR * r)) << 4), Vb + src);
       }
     };
-    if (warp < ntiles) {
-      load_k(warp);
-      load_v(warp);
+#pragma unroll
+    for (int s = 0; s < kKv8Stages - 1; ++s) {
+      if (s < my_n) issue(s);
+      cp_async_commit();
     }
-    for (int tile = warp; tile < ntiles; tile += kAttnWarps) {
-      const bool more = tile + kAttnWarps < ntiles;
-      // ---- S^T = K Q^T: s[0..1] = token grp, s[2..3] = token grp + 8; heads 2tq + {0,1}
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (sc0 == t0) load_q_f16<D, GS>(p.q, (size_t)b * p.Hq + g * GS, grp, tq, qb, qs);
+    for (int it = 0; it < my_n; ++it) {
+      __syncwarp();  // the stage refilled now has been read by every lane
+      if (it + kKv8Stages - 1 < my_n) issue(it + kKv8Stages - 1);
+      cp_async_commit();
+      cp_async_wait<kKv8Stages - 1>();
+      __syncwarp();  // the pieces come from other lanes
+      const uint32_t off = (uint32_t)(it % kKv8Stages) * STAGE;
+      const int base = (warp + it * kAttnWarps) * kKv8Tok;
+      // ---- S^T = K Q^T: s[u][0..1] = token 16u + grp, s[u][2..3] = 16u + grp + 8; heads 2tq + {0,1}
+      float s[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < KLD; ++i) {
-        const uint32_t wa[4] = {kc[0][i].x, kc[0][i].y, kc[0][i].z, kc[0][i].w};
-        const uint32_t wb[4] = {kc[1][i].x, kc[1][i].y, kc[1][i].z, kc[1][i].w};
+        uint32_t w[U][2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t a0, a1, a2, a3;
-          kv8_to_f16<FMT>(wa[j], a0, a2);
-          kv8_to_f16<FMT>(wb[j], a1, a3);
-          mma_16816_f16(s, a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
+        for (int u = 0; u < U; ++u) {
+          const uint32_t at = k_src + off + 16 * u * D + (((tq + 4 * i) ^ kv8_swizzle_k<D>(grp)) << 4);
+          const uint4 ka = lds16(at), kb = lds16(at + 8 * D);  // rows grp, grp + 8
+          w[u][0][0] = ka.x; w[u][0][1] = ka.y; w[u][0][2] = ka.z; w[u][0][3] = ka.w;
+          w[u][1][0] = kb.x; w[u][1][1] = kb.y; w[u][1][2] = kb.z; w[u][1][3] = kb.w;
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            uint32_t a0, a1, a2, a3;
+            kv8_to_f16<FMT>(w[u][0][j], a0, a2);
+            kv8_to_f16<FMT>(w[u][1][j], a1, a3);
+            mma_16816_f16(s[u], a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
+          }
       }
-      if (more) load_k(tile + kAttnWarps);
-      const uint32_t e0 = list_hb[tile * kAttnTile + grp], e1 = list_hb[tile * kAttnTile + grp + 8];
-      const float2 c0 = tab[e0 >> 8], c1 = tab[e1 >> 8];
-      const uint32_t hb0 = (e0 & 0xFFu) >> (2 * tq) & head_bits, hb1 = (e1 & 0xFFu) >> (2 * tq) & head_bits;
-      float x[4];
-      x[0] = (hb0 & 1u) ? s[0] * qs[0] * c0.x : kNegInf;
-      x[1] = (hb0 & 2u) ? s[1] * qs[1] * c0.x : kNegInf;
-      x[2] = (hb1 & 1u) ? s[2] * qs[0] * c1.x : kNegInf;
-      x[3] = (hb1 & 2u) ? s[3] * qs[1] * c1.x : kNegInf;
-      const float y[4] = {x[0] + c0.y, x[1] + c0.y, x[2] + c1.y, x[3] + c1.y};
-      float mt[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-      float rt[2] = {fmaxf(y[0], y[2]), fmaxf(y[1], y[3])};
+      float x[U][4], y[U][4];
+      float mt[2] = {kNegInf, kNegInf}, rt[2] = {kNegInf, kNegInf};
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float2 c[2];     // of tokens grp and grp + 8
+        uint32_t hb[2];  // the lane's two heads
+        if constexpr (DENSE) {
+          const uint2 sc = lds8(scales + (it % kKv8Stages) * 8 * U + 8 * u);
+          const float ks = __uint_as_float(sc.x);
+          c[0] = c[1] = make_float2(ks * p.scale_log2, __log2f(__uint_as_float(sc.y)));
+          const int left = ks == ks ? n - base - 16 * u : 0;
+          hb[0] = grp < left ? head_bits : 0u;
+          hb[1] = grp + 8 < left ? head_bits : 0u;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t e = list_hb[base + 16 * u + grp + 8 * r];
+            c[r] = tab[e >> 8];
+            hb[r] = (e & 0xFFu) >> (2 * tq) & head_bits;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // a masked token's weight is zero whatever its block's scale says
+            const bool in = hb[r] >> e & 1u;
+            x[u][2 * r + e] = in ? s[u][2 * r + e] * qs[e] * c[r].x : kNegInf;
+            y[u][2 * r + e] = in ? x[u][2 * r + e] + c[r].y : kNegInf;
+            mt[e] = fmaxf(mt[e], x[u][2 * r + e]);
+            rt[e] = fmaxf(rt[e], y[u][2 * r + e]);
+          }
+      }
       const bool over = mt[0] > m_run[0] + 8.f || mt[1] > m_run[1] + 8.f || rt[0] > r_run[0] + 8.f ||
                         rt[1] > r_run[1] + 8.f;
       if (__any_sync(0xffffffffu, over)) {
@@ -360,30 +493,59 @@ __global__ void __launch_bounds__(kAttnThreads, 4) attn_kv8_kernel(const AttnKv8
         }
       }
       // a head with no kept token so far subtracts 0: every exponent is -inf
-      const float mu0 = m_run[0] == kNegInf ? 0.f : m_run[0], mu1 = m_run[1] == kNegInf ? 0.f : m_run[1];
-      const float ru0 = r_run[0] == kNegInf ? 0.f : r_run[0] - 7.f, ru1 = r_run[1] == kNegInf ? 0.f : r_run[1] - 7.f;
-      l_run[0] += fast_exp2(x[0] - mu0) + fast_exp2(x[2] - mu0);
-      l_run[1] += fast_exp2(x[1] - mu1) + fast_exp2(x[3] - mu1);
-      const uint32_t pb0 = movmatrix_trans(pack_f16(fast_exp2(y[0] - ru0), fast_exp2(y[1] - ru1)));
-      const uint32_t pb1 = movmatrix_trans(pack_f16(fast_exp2(y[2] - ru0), fast_exp2(y[3] - ru1)));
+      float mu[2], ru[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mu[e] = m_run[e] == kNegInf ? 0.f : m_run[e];
+        ru[e] = r_run[e] == kNegInf ? 0.f : r_run[e] - 7.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) l_run[e] += fast_exp2(x[u][e] - mu[e]) + fast_exp2(x[u][2 + e] - mu[e]);
+      }
+      uint32_t pb[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          pb[u][r] = movmatrix_trans(pack_f16(fast_exp2(y[u][2 * r] - ru[0]), fast_exp2(y[u][2 * r + 1] - ru[1])));
       // ---- O^T += V^T P^T
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
+      for (int u = 0; u < U; ++u) {
+        uint32_t vc[4][VW];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // bytes 2h and 2h + 1 of the word: m-tile 2j + h
-          const uint32_t sel = h ? 0x7362 : 0x5140;
-          uint32_t a0, a1, a2, a3;
-          kv8_to_f16<FMT>(__byte_perm(vc[0][j], vc[1][j], sel), a0, a1);
-          kv8_to_f16<FMT>(__byte_perm(vc[2][j], vc[3][j], sel), a2, a3);
-          mma_16816_f16(o[2 * j + h], a0, a1, a2, a3, pb0, pb1);
+        for (int r = 0; r < 4; ++r) {
+          const int row = (r & 1) + 8 * (r >> 1);  // + 2tq
+          const uint32_t at = v_src + off + (16 * u + row) * D + (((grp * VB >> 4) ^ kv8_swizzle_v<D>(2 * tq + row)) << 4);
+          if constexpr (VW == 4) {
+            const uint4 v = lds16(at);
+            vc[r][0] = v.x;
+            vc[r][1] = v.y;
+            vc[r][2] = v.z;
+            vc[r][3] = v.w;
+          } else {
+            const uint2 v = lds8(at);
+            vc[r][0] = v.x;
+            vc[r][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // bytes 2h and 2h + 1 of the word: m-tile 2j + h
+            const uint32_t sel = h ? 0x7362 : 0x5140;
+            uint32_t a0, a1, a2, a3;
+            kv8_to_f16<FMT>(__byte_perm(vc[0][j], vc[1][j], sel), a0, a1);
+            kv8_to_f16<FMT>(__byte_perm(vc[2][j], vc[3][j], sel), a2, a3);
+            mma_16816_f16(o[2 * j + h], a0, a1, a2, a3, pb[u][0], pb[u][1]);
+          }
         }
       }
-      if (more) load_v(tile + kAttnWarps);
     }
-    __syncthreads();  // the gather list is free for the next sub-chunk
+    cp_async_wait<0>();
+    if (!DENSE) __syncthreads();  // the gather list is free for the next sub-chunk
   }
 
-  // ---- merge the four warps through shared memory (the list's)
+  // ---- merge the four warps through shared memory (reuses the ring)
+  __syncthreads();
   float* wm = reinterpret_cast<float*>(smem);
   float* wl = wm + kAttnWarps * GS;
   float* wo = wl + kAttnWarps * GS;

@@ -402,8 +402,10 @@ static tb_status launch_select(tb_ctx* ctx, int layer, const float* scores, bool
 // The split attention kernel over an 8-bit layer (the partials' combine is the caller's).
 template <int F, int D, int GS>
 static tb_status launch_attn_kv8_as(bool bf16, const AttnKv8Params& p, dim3 grid, cudaStream_t st) {
-  auto k = bf16 ? attn_kv8_kernel<F, D, GS> : attn_kv8_f32_kernel<F, D, GS>;
-  const int smem = bf16 ? attn_kv8_smem<D, GS>() : attn_kv8_f32_smem<D, GS>();
+  const bool dense = p.mask_mode == TB_MASK_DENSE;
+  auto k = !bf16 ? attn_kv8_f32_kernel<F, D, GS> : dense ? attn_kv8_kernel<F, D, GS, true> : attn_kv8_kernel<F, D, GS, false>;
+  const int smem = !bf16 ? attn_kv8_f32_smem<D, GS>()
+                         : dense ? attn_kv8_smem<D, GS, true>() : attn_kv8_smem<D, GS, false>();
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TB_ERR_CUDA;
   launch_pdl(k, grid, dim3(kAttnThreads), smem, st, p);
   return cuda_status(cudaGetLastError());
@@ -450,7 +452,10 @@ static tb_status launch_attn(tb_ctx* ctx, int layer, const void* q, const uint32
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
   for (int b = 0; b < c.batch; ++b) p.lens[b] = ls.lens[b];
   int chunk = 0;
-  if (!attn_split(ctx->num_sms, c.batch * c.n_kv_heads, maxL, &chunk, &p.nsplit)) return TB_ERR_UNSUPPORTED;
+  if (ls.kv8)
+    attn_split_kv8(ctx->num_sms, c.n_kv_heads, ls.lens, c.batch, ctx->lay.max_splits, &chunk, &p.nsplit);
+  else if (!attn_split(ctx->num_sms, c.batch * c.n_kv_heads, maxL, &chunk, &p.nsplit))
+    return TB_ERR_UNSUPPORTED;
   p.chunk = chunk;
   if (p.nsplit > ctx->lay.max_splits) return TB_ERR_WORKSPACE;
   {
