@@ -18,11 +18,15 @@ struct AttnKv8Params : AttnParams {
   const float* v_scale;
 };
 
-// Split of the 8-bit attention (host side): the shortest chunks (whole mask
-// words) that keep all of the call's CTAs in one wave of kKv8CtasPerSm per SM,
-// counting the tokens that each sequence has.
+// Split of the 8-bit attention (host side), counting the tokens that each
+// sequence has: the shortest chunks (whole mask words) that keep the call's CTAs
+// within one wave of kKv8CtasPerSm per SM, or, where these would be longer than
+// kKv8LongChunk, within as many waves as bring them down to it (dense B = 4, L =
+// 131072: 203 us in one wave of 7296 tokens, 183 us with 2048; short chunks in
+// several waves lose: B = 16, L = 8192, 66 us either way).
 constexpr int kKv8CtasPerSm = 4;
 constexpr int kKv8MinChunk = 128;
+constexpr int kKv8LongChunk = 2048;
 inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch, int max_splits, int* chunk_out,
                            int* nsplit_out) {
   long long total = 0;
@@ -31,7 +35,9 @@ inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch
     total += lens[b];
     longest = lens[b] > longest ? lens[b] : longest;
   }
-  const long long slots = (long long)kKv8CtasPerSm * num_sms;
+  const long long wave = (long long)kKv8CtasPerSm * num_sms;
+  const long long one = (total * kv_heads + wave - 1) / wave;  // the chunk of one wave
+  const long long slots = wave * ((one + kKv8LongChunk - 1) / kKv8LongChunk > 0 ? (one + kKv8LongChunk - 1) / kKv8LongChunk : 1);
   long long chunk = (total * kv_heads + slots - 1) / slots;
   const long long least = (longest + max_splits - 1) / max_splits;
   chunk = chunk < least ? least : chunk;
@@ -231,18 +237,22 @@ __device__ __forceinline__ void load_q_f16(const void* q, size_t head0, int grp,
   qs[1] = kv8_pow2(-__shfl_sync(0xffffffffu, up, (8 * tq + 4) & 31));
 }
 
-// Ring of one warp: kKv8Stages stages of 32 tokens.
+// Ring of one warp: kKv8Stages tiles of 16 K and V rows.
 constexpr int kKv8Stages = 3;
-constexpr int kKv8Tok = 16;       // tokens of an iteration
-constexpr int kKv8MaxList = 1024; // tokens per gather list
+constexpr int kKv8Seg = 256;  // tokens of a warp's gather list
 template <int D>
-constexpr int kv8_stage_bytes() { return 2 * kKv8Tok * D; }
+constexpr int kv8_stage_bytes() { return 2 * kAttnTile * D; }
+// per warp: the ring, per stage the tokens' (ks, log2 vs, head bits), and for a
+// list its entries and the segment's blocks
+template <int D, bool DENSE>
+constexpr int attn_kv8_warp_bytes() {
+  return kKv8Stages * (kv8_stage_bytes<D>() + kAttnTile * 16) + (DENSE ? 0 : kKv8Seg * 2 + kKv8Seg / kKv8Block * 16);
+}
 template <int D, int GS, bool DENSE>
 constexpr int attn_kv8_smem() {
-  constexpr int ring = kAttnWarps * kKv8Stages * (kv8_stage_bytes<D>() + (DENSE ? kKv8Tok / 2 : 0));
-  constexpr int list = DENSE ? 0 : (kKv8MaxList + kKv8Tok) * 6 + (kKv8MaxList / kKv8Block) * 8;
+  constexpr int work = kAttnWarps * attn_kv8_warp_bytes<D, DENSE>();
   constexpr int merge = kAttnWarps * GS * (D + 2) * 4;
-  return ring + list > merge ? ring + list : merge;
+  return work > merge ? work : merge;
 }
 // 16-byte pieces of a cached row are stored at piece ^ swizzle(row), so that the
 // lanes of a shared-memory phase touch different banks: for K two rows' pieces
@@ -278,16 +288,18 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 //  - V: it takes D/8 bytes (dims grp D/8 ..) of token rows 2tq, 2tq+1, 2tq+8,
 //    2tq+9; byte permutes pair the tokens of a dim, and m-tile mt takes dims
 //    grp D/8 + 2mt and + 2mt + 1 as its rows grp and grp + 8.
-// Two tiles an iteration: their products and conversions are independent, which
-// a warp needs more than bytes in flight (one tile at a time was a chain of about
-// 2100 cycles).  A ring of kKv8Stages iterations per warp holds the loads.  Rows
-// are copied whole (eight lanes a 128-byte row: four lanes that took a sector each of
-// four rows made L2 send half as much again).
+// A ring of kKv8Stages tiles per warp holds the loads.  Rows are copied whole
+// (eight lanes a 128-byte row: requests that took one sector of each of four rows
+// made L2 send half as much again).
 //
-// DENSE takes every token of the chunk: tiles are blocks of the cache, so one
-// row lookup and one scale pair serve a tile and there is no gather list.
-// Otherwise the union of the group's masks is listed as in attn_bf16_kernel,
-// with each token's block in the sub-chunk beside its head bits.
+// DENSE takes every token of the chunk, tiles in turn over the warps: a tile is
+// one block of the cache, so one row lookup and one scale pair serve it.
+// Otherwise each warp walks its quarter of the chunk in segments of kKv8Seg
+// tokens: it lists the union of the group's masks (8 tokens a lane), with the
+// next segment's words, rows and scales already requested, and cuts the list
+// into tiles; tokens that do not fill a tile wait in registers for the next
+// segment's.  No barrier joins the warps, and the ring does not drain between
+// segments (a CTA-wide list cost 40 % of the stalls).
 //
 // Softmax (log2 domain, fp32): l sums p = 2^(x - m); the weights of the V
 // codes are w = 2^(x + log2 vs - r + 7) with their own running exponent r, so
@@ -304,13 +316,9 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   constexpr int KSTEPS = D / 16, MT = D / 16;
   constexpr int KLD = D / 64;                   // 16-byte pieces of a K row per lane
   constexpr int VW = D / 32, VB = D / 8;        // words and bytes of a V row per lane
-  constexpr int U = kKv8Tok / 16;               // mma tiles of an iteration
-  constexpr int VOFF = kKv8Tok * D;             // V slots of a stage
+  constexpr int VOFF = kAttnTile * D;           // V rows of a stage
   constexpr int STAGE = kv8_stage_bytes<D>();
   extern __shared__ __align__(128) uint8_t smem[];
-  int32_t* list_idx = reinterpret_cast<int32_t*>(smem + kAttnWarps * kKv8Stages * STAGE);
-  float2* tab = reinterpret_cast<float2*>(list_idx + kKv8MaxList + kKv8Tok);  // per block: ks log2e/sqrt(D), log2 vs
-  uint16_t* list_hb = reinterpret_cast<uint16_t*>(tab + kKv8MaxList / kKv8Block);
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int L = p.lens[b];
   const int t0 = split * p.chunk;
@@ -324,10 +332,11 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   const int c_row = lane / NPC, c_part = lane % NPC;
   const uint8_t* Kb = reinterpret_cast<const uint8_t*>(p.k_cache) + 16 * c_part;
   const uint8_t* Vb = reinterpret_cast<const uint8_t*>(p.v_cache) + 16 * c_part;
-  const uint32_t ring = smem_u32(smem) + warp * kKv8Stages * STAGE;
+  uint8_t* mine = smem + warp * attn_kv8_warp_bytes<D, DENSE>();
+  const uint32_t ring = smem_u32(mine);
   const uint32_t c_dst = ring + c_row * D, k_src = ring + grp * D, v_src = ring + VOFF + 2 * tq * D + grp * VB % 16;
-  // DENSE: per stage, the (ks, vs) pairs of its two blocks
-  const uint32_t scales = smem_u32(smem) + kAttnWarps * kKv8Stages * STAGE + warp * kKv8Stages * 8 * U;
+  // per stage: DENSE: the block's (ks, vs); else the 16 tokens' (ks log2e/sqrt(D), log2 vs, head bits)
+  const uint32_t meta = ring + kKv8Stages * STAGE;
 
   uint32_t qb[KSTEPS][2];
   float qs[2];
@@ -337,212 +346,285 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   float m_run[2] = {kNegInf, kNegInf}, r_run[2] = {kNegInf, kNegInf}, l_run[2] = {0.f, 0.f};
 
-  for (int sc0 = t0, sc1; sc0 < t1; sc0 = sc1) {
-    sc1 = DENSE ? t1 : min(sc0 + kKv8MaxList, t1);  // one gather list each
-    int n = sc1 - sc0;
-    if constexpr (!DENSE) {
-      __shared__ uint32_t scan_sm[32];
-      // the sub-chunk's block scales: at most one block per thread
-      const int t = sc0 + tid * kKv8Block;
+
+  // copies of a tile's 16 rows (of cache rows rows[r] = that of token c_row + CR r)
+  auto copy_rows = [&](uint32_t off, const uint32_t (&rows)[kAttnTile / CR]) {
+#pragma unroll
+    for (int r = 0; r < kAttnTile / CR; ++r) {
+      const size_t src = (size_t)rows[r] * D;
+      const uint32_t dst = c_dst + off + r * CR * D;
+      cp_async_16u(dst + ((c_part ^ kv8_swizzle_k<D>(c_row + CR * r)) << 4), Kb + src);
+      cp_async_16u(dst + VOFF + ((c_part ^ kv8_swizzle_v<D>(c_row + CR * r)) << 4), Vb + src);
+    }
+  };
+
+  // ---- the warp's tiles: issue(it) starts the copies of tile `it`, false when there is none
+  const int dense_tiles = (t1 - t0 + kAttnTile - 1) / kAttnTile;
+  // list state: the segment being cut (list entries [pos, cnt)), the waiting tokens
+  // (lanes 0 .. wait_n - 1), the next segment [seg, seg_end) and what is requested of it
+  uint16_t* list = reinterpret_cast<uint16_t*>(mine + kKv8Stages * (STAGE + kAttnTile * 16));
+  uint4* blocks = reinterpret_cast<uint4*>(list + kKv8Seg);  // (row, ks log2e/sqrt(D), log2 vs) of a segment's blocks
+  constexpr int MW = (GS * (kKv8Seg / 32) + 31) / 32;        // mask words a lane requests
+  const int quarter = ((t1 - t0 + kAttnWarps - 1) / kAttnWarps + 31) / 32 * 32;
+  int seg = min(t0 + warp * quarter, t1);
+  const int seg_end = min(seg + quarter, t1);
+  int pos = 0, cnt = 0, wait_n = 0;
+  uint32_t w_row = 0, w_hb = 0, n_word[MW], n_row = 0;
+  float w_ks = 0.f, w_ev = 0.f, n_scale = 0.f;
+  bool n_ok = true;
+  const bool per_head = p.mask_mode == TB_MASK_PER_HEAD;
+  auto request = [&]() {  // segment [seg, ..): its mask words, and lane l's block l % 16 (row; ks below lane 16, vs above)
+#pragma unroll
+    for (int i = 0; i < MW; ++i) {
+      const int e = lane + 32 * i, h = e / (kKv8Seg / 32), w = e % (kKv8Seg / 32);
+      n_word[i] = 0u;
+      if (seg + 32 * w < seg_end && (per_head ? h < GS : h == 0)) {
+        const size_t row = per_head ? (size_t)b * p.Hq + g * GS + h
+                                    : p.mask_mode == TB_MASK_GROUP ? (size_t)b * p.Hkv + g : (size_t)b;
+        n_word[i] = p.mask[row * p.mask_words + (seg >> 5) + w];
+      }
+    }
+    const int t = seg + (lane & 15) * kKv8Block;
+    n_ok = true;
+    if (t < seg_end) {
+      n_ok = kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &n_row);
+      n_scale = (lane < 16 ? p.k_scale : p.v_scale)[n_row >> 4];
+    }
+  };
+  auto build = [&]() {  // lists the requested segment and requests the next one
+    __syncwarp();       // the previous list has been read
+    const int w = lane >> 2, sh = 8 * (lane & 3);
+    uint32_t byte[GS], u = 0;  // per head, the mask bits of the lane's 8 tokens
+#pragma unroll
+    for (int h = 0; h < GS; ++h) {
+      const int e = (per_head ? h : 0) * (kKv8Seg / 32) + w;
+      uint32_t v = __shfl_sync(0xffffffffu, n_word[0], e & 31);
+      if (MW > 1) {
+        const uint32_t v1 = __shfl_sync(0xffffffffu, n_word[MW - 1], e & 31);
+        v = e < 32 ? v : v1;
+      }
+      byte[h] = v >> sh & 0xFFu;
+      u |= byte[h];
+    }
+    const int valid = seg_end - (seg + 8 * lane);
+    if (valid < 8) u &= valid > 0 ? (1u << valid) - 1u : 0u;
+    const bool ok = __shfl_sync(0xffffffffu, n_ok, lane >> 1);
+    if (!ok && u) {
+      atomicOr(p.status, TB_DEV_ERR_INDEX);
+      u = 0u;
+    }
+    const uint32_t c = __popc(u);
+    uint32_t incl = c;
+#pragma unroll
+    for (int o2 = 1; o2 < 32; o2 <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o2);
+      if (lane >= o2) incl += y;
+    }
+    uint16_t* at = list + (incl - c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (u >> j & 1u) {
+        uint32_t hb = 0;
+#pragma unroll
+        for (int h = 0; h < GS; ++h) hb |= (byte[h] >> j & 1u) << h;
+        *at++ = (uint16_t)((8 * lane + j) | hb << 8);
+      }
+    }
+    const float vs = __shfl_sync(0xffffffffu, n_scale, (lane & 15) + 16);
+    if (lane < 16)
+      blocks[lane] = make_uint4(n_row, __float_as_uint(n_scale * p.scale_log2), __float_as_uint(__log2f(vs)), 0u);
+    cnt = (int)__shfl_sync(0xffffffffu, incl, 31);
+    pos = 0;
+    seg += kKv8Seg;
+    if (seg < seg_end) request();
+    __syncwarp();
+  };
+  // lane's token of the list, entry i
+  auto entry = [&](int i, uint32_t& row, float& ks, float& ev, uint32_t& hb) {
+    const uint32_t v = list[i];
+    const uint4 blk = blocks[(v & 0xFFu) >> 4];
+    row = blk.x + (v & 15u);
+    ks = __uint_as_float(blk.y);
+    ev = __uint_as_float(blk.z);
+    hb = v >> 8;
+  };
+  auto issue = [&](int it) -> bool {
+    const uint32_t stage = (uint32_t)(it % kKv8Stages);
+    uint32_t rows[kAttnTile / CR];
+    if constexpr (DENSE) {
+      const int tile = warp + it * kAttnWarps;
+      if (tile >= dense_tiles) return false;
+      const int tt = t0 + tile * kAttnTile;
       uint32_t row;
-      if (t < sc1 && kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &row))
-        tab[tid] = make_float2(p.k_scale[row >> 4] * p.scale_log2, __log2f(p.v_scale[row >> 4]));
-      n = build_union<GS, kKv8MaxList, kKv8Tok>(p, b, g, sc0, sc1, scan_sm, [&](int pos, int tt, uint32_t hb) {
-        uint32_t rr;
-        if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, tt, &rr)) {
-          atomicOr(p.status, TB_DEV_ERR_INDEX);
-          hb = 0u;
-        }
-        list_idx[pos] = (int32_t)rr;
-        list_hb[pos] = (uint16_t)(hb | (uint32_t)(tt - sc0) / kKv8Block << 8);
-      });
+      const bool ok = kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, tt, &row);
+      const int last = ok ? t1 - 1 - tt : 0;  // rows past the end repeat the last one
+      const uint32_t dst = meta + stage * (kAttnTile * 16);
+      if (ok) {  // one lane per scale: a request fetches a sector for each active lane
+        if (lane == 0) cp_async_4(dst, p.k_scale + (row >> 4));
+        if (lane == 1) cp_async_4(dst + 4, p.v_scale + (row >> 4));
+      } else if (lane == 0) {  // a page outside the pool: the block's scale is NaN
+        atomicOr(p.status, TB_DEV_ERR_INDEX);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(0x7fffffff) : "memory");
+      }
+#pragma unroll
+      for (int r = 0; r < kAttnTile / CR; ++r) rows[r] = row + min(c_row + CR * r, last);
+    } else {
+      const int l16 = lane & 15;
+      while (wait_n + cnt - pos < kAttnTile && seg < seg_end) {
+        if (l16 >= wait_n && l16 < wait_n + cnt - pos) entry(pos + l16 - wait_n, w_row, w_ks, w_ev, w_hb);
+        wait_n += cnt - pos;
+        build();
+      }
+      const int n = min(wait_n + cnt - pos, kAttnTile);
+      if (n == 0) return false;
+      uint32_t row = w_row, hb = w_hb;
+      float ks = w_ks, ev = w_ev;
+      if (l16 >= wait_n && l16 < n) entry(pos + l16 - wait_n, row, ks, ev, hb);
+      pos += n - wait_n;
+      wait_n = 0;
+      const uint32_t first = __shfl_sync(0xffffffffu, row, 0);
+      if (l16 >= n) {  // past the last token: its row again, for no head
+        row = first;
+        ks = ev = 0.f;
+        hb = 0u;
+      }
+      if (lane < 16)
+        *reinterpret_cast<uint4*>(mine + kKv8Stages * STAGE + (stage * kAttnTile + lane) * 16) =
+            make_uint4(__float_as_uint(ks), __float_as_uint(ev), hb, 0u);
+#pragma unroll
+      for (int r = 0; r < kAttnTile / CR; ++r) rows[r] = __shfl_sync(0xffffffffu, row, c_row + CR * r);
     }
-    const int niter = (n + kKv8Tok - 1) / kKv8Tok;
-    const int my_n = niter > warp ? (niter - warp + kAttnWarps - 1) / kAttnWarps : 0;
-    auto issue = [&](int it) {
-      const int base = (warp + it * kAttnWarps) * kKv8Tok;
-      const uint32_t off = (uint32_t)(it % kKv8Stages) * STAGE;
-      uint32_t rows[kKv8Tok / CR];
-      if constexpr (DENSE) {
-        uint32_t row[U];
-        int last[U];  // rows past the end repeat the last one
+    copy_rows(stage * STAGE, rows);
+    return true;
+  };
+
+  if (!DENSE && seg < seg_end) request();
+  int queued = 0;  // tiles whose copies have started
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int tt = sc0 + base + 16 * u;
-          const bool in = tt < sc1;
-          const bool ok = kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, in ? tt : sc0 + base, &row[u]);
-          last[u] = ok && in ? sc1 - 1 - tt : 0;
-          const uint32_t dst = scales + (it % kKv8Stages) * 8 * U + 8 * u;
-          if (ok) {
-            if (lane == 0) cp_async_4(dst, p.k_scale + (row[u] >> 4));
-            if (lane == 1) cp_async_4(dst + 4, p.v_scale + (row[u] >> 4));
-          } else if (lane == 0) {  // a page outside the pool: the block's scale is NaN
-            atomicOr(p.status, TB_DEV_ERR_INDEX);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(0x7fffffff) : "memory");
-          }
-        }
+  for (int s = 0; s < kKv8Stages - 1; ++s) {
+    if (issue(s)) ++queued;
+    cp_async_commit();
+  }
+  load_q_f16<D, GS>(p.q, (size_t)b * p.Hq + g * GS, grp, tq, qb, qs);
+  for (int it = 0; it < queued; ++it) {
+    __syncwarp();  // the stage refilled now has been read by every lane
+    if (queued == it + kKv8Stages - 1 && issue(queued)) ++queued;
+    cp_async_commit();
+    cp_async_wait<kKv8Stages - 1>();
+    __syncwarp();  // the pieces come from other lanes
+    const uint32_t stage = (uint32_t)(it % kKv8Stages), off = stage * STAGE;
+    // ---- S^T = K Q^T: s[0..1] = token grp, s[2..3] = grp + 8; heads 2tq + {0,1}
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < kKv8Tok / CR; ++r) {
-          const int u = r * CR / 16;
-          rows[r] = row[u] + min(c_row + CR * r - 16 * u, last[u]);
-        }
-      } else {
+    for (int i = 0; i < KLD; ++i) {
+      const uint32_t at = k_src + off + (((tq + 4 * i) ^ kv8_swizzle_k<D>(grp)) << 4);
+      const uint4 ka = lds16(at), kb = lds16(at + 8 * D);  // rows grp, grp + 8
+      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int r = 0; r < kKv8Tok / CR; ++r) rows[r] = (uint32_t)list_idx[base + c_row + CR * r];
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a0, a1, a2, a3;
+        kv8_to_f16<FMT>(wa[j], a0, a2);
+        kv8_to_f16<FMT>(wb[j], a1, a3);
+        mma_16816_f16(s, a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
       }
-#pragma unroll
-      for (int r = 0; r < kKv8Tok / CR; ++r) {
-        const size_t src = (size_t)rows[r] * D;
-        const uint32_t dst = c_dst + off + r * CR * D;
-        cp_async_16u(dst + ((c_part ^ kv8_swizzle_k<D>(c_row + CR * r)) << 4), Kb + src);
-        cp_async_16u(dst + VOFF + ((c_part ^ kv8_swizzle_v<D>(c_row + CR * r)) << 4), Vb + src);
-      }
-    };
-#pragma unroll
-    for (int s = 0; s < kKv8Stages - 1; ++s) {
-      if (s < my_n) issue(s);
-      cp_async_commit();
     }
-    if (sc0 == t0) load_q_f16<D, GS>(p.q, (size_t)b * p.Hq + g * GS, grp, tq, qb, qs);
-    for (int it = 0; it < my_n; ++it) {
-      __syncwarp();  // the stage refilled now has been read by every lane
-      if (it + kKv8Stages - 1 < my_n) issue(it + kKv8Stages - 1);
-      cp_async_commit();
-      cp_async_wait<kKv8Stages - 1>();
-      __syncwarp();  // the pieces come from other lanes
-      const uint32_t off = (uint32_t)(it % kKv8Stages) * STAGE;
-      const int base = (warp + it * kAttnWarps) * kKv8Tok;
-      // ---- S^T = K Q^T: s[u][0..1] = token 16u + grp, s[u][2..3] = 16u + grp + 8; heads 2tq + {0,1}
-      float s[U][4];
+    float2 c[2];     // of tokens grp and grp + 8: ks log2e/sqrt(D), log2 vs
+    uint32_t hb[2];  // their bits of the lane's two heads
+    if constexpr (DENSE) {
+      const uint2 sc = lds8(meta + stage * (kAttnTile * 16));
+      const float ks = __uint_as_float(sc.x);
+      c[0] = c[1] = make_float2(ks * p.scale_log2, __log2f(__uint_as_float(sc.y)));
+      const int left = ks == ks ? t1 - t0 - (warp + it * kAttnWarps) * kAttnTile : 0;
+      hb[0] = grp < left ? head_bits : 0u;
+      hb[1] = grp + 8 < left ? head_bits : 0u;
+    } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
-#pragma unroll
-      for (int i = 0; i < KLD; ++i) {
-        uint32_t w[U][2][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t at = k_src + off + 16 * u * D + (((tq + 4 * i) ^ kv8_swizzle_k<D>(grp)) << 4);
-          const uint4 ka = lds16(at), kb = lds16(at + 8 * D);  // rows grp, grp + 8
-          w[u][0][0] = ka.x; w[u][0][1] = ka.y; w[u][0][2] = ka.z; w[u][0][3] = ka.w;
-          w[u][1][0] = kb.x; w[u][1][1] = kb.y; w[u][1][2] = kb.z; w[u][1][3] = kb.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            uint32_t a0, a1, a2, a3;
-            kv8_to_f16<FMT>(w[u][0][j], a0, a2);
-            kv8_to_f16<FMT>(w[u][1][j], a1, a3);
-            mma_16816_f16(s[u], a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
-          }
+      for (int r = 0; r < 2; ++r) {
+        const uint4 e = lds16(meta + (stage * kAttnTile + grp + 8 * r) * 16);
+        c[r] = make_float2(__uint_as_float(e.x), __uint_as_float(e.y));
+        hb[r] = e.z >> (2 * tq) & head_bits;
       }
-      float x[U][4], y[U][4];
-      float mt[2] = {kNegInf, kNegInf}, rt[2] = {kNegInf, kNegInf};
+    }
+    float x[4], y[4];
+    float mt[2], rt[2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float2 c[2];     // of tokens grp and grp + 8
-        uint32_t hb[2];  // the lane's two heads
-        if constexpr (DENSE) {
-          const uint2 sc = lds8(scales + (it % kKv8Stages) * 8 * U + 8 * u);
-          const float ks = __uint_as_float(sc.x);
-          c[0] = c[1] = make_float2(ks * p.scale_log2, __log2f(__uint_as_float(sc.y)));
-          const int left = ks == ks ? n - base - 16 * u : 0;
-          hb[0] = grp < left ? head_bits : 0u;
-          hb[1] = grp + 8 < left ? head_bits : 0u;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t e = list_hb[base + 16 * u + grp + 8 * r];
-            c[r] = tab[e >> 8];
-            hb[r] = (e & 0xFFu) >> (2 * tq) & head_bits;
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // a masked token's weight is zero whatever its block's scale says
-            const bool in = hb[r] >> e & 1u;
-            x[u][2 * r + e] = in ? s[u][2 * r + e] * qs[e] * c[r].x : kNegInf;
-            y[u][2 * r + e] = in ? x[u][2 * r + e] + c[r].y : kNegInf;
-            mt[e] = fmaxf(mt[e], x[u][2 * r + e]);
-            rt[e] = fmaxf(rt[e], y[u][2 * r + e]);
-          }
-      }
-      const bool over = mt[0] > m_run[0] + 8.f || mt[1] > m_run[1] + 8.f || rt[0] > r_run[0] + 8.f ||
-                        rt[1] > r_run[1] + 8.f;
-      if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) {
-            mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], sh));
-            rt[e] = fmaxf(rt[e], __shfl_xor_sync(0xffffffffu, rt[e], sh));
-          }
-          const float mn = fmaxf(m_run[e], mt[e]), rn = fmaxf(r_run[e], rt[e]);
-          // a head with no token so far has l = 0 and o = 0: any factor serves
-          l_run[e] *= m_run[e] == mn ? 1.f : fast_exp2(m_run[e] - mn);
-          const float al = r_run[e] == rn ? 1.f : fast_exp2(r_run[e] - rn);
-          m_run[e] = mn;
-          r_run[e] = rn;
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            o[j][e] *= al;
-            o[j][2 + e] *= al;
-          }
-        }
-      }
-      // a head with no kept token so far subtracts 0: every exponent is -inf
-      float mu[2], ru[2];
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mu[e] = m_run[e] == kNegInf ? 0.f : m_run[e];
-        ru[e] = r_run[e] == kNegInf ? 0.f : r_run[e] - 7.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) l_run[e] += fast_exp2(x[u][e] - mu[e]) + fast_exp2(x[u][2 + e] - mu[e]);
+        // a masked token's weight is zero whatever its block's scale says
+        const bool in = hb[r] >> e & 1u;
+        x[2 * r + e] = in ? s[2 * r + e] * qs[e] * c[r].x : kNegInf;
+        y[2 * r + e] = in ? x[2 * r + e] + c[r].y : kNegInf;
       }
-      uint32_t pb[U][2];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+    for (int e = 0; e < 2; ++e) {
+      mt[e] = fmaxf(x[e], x[2 + e]);
+      rt[e] = fmaxf(y[e], y[2 + e]);
+    }
+    const bool over = mt[0] > m_run[0] + 8.f || mt[1] > m_run[1] + 8.f || rt[0] > r_run[0] + 8.f ||
+                      rt[1] > r_run[1] + 8.f;
+    if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          pb[u][r] = movmatrix_trans(pack_f16(fast_exp2(y[u][2 * r] - ru[0]), fast_exp2(y[u][2 * r + 1] - ru[1])));
-      // ---- O^T += V^T P^T
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t vc[4][VW];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = (r & 1) + 8 * (r >> 1);  // + 2tq
-          const uint32_t at = v_src + off + (16 * u + row) * D + (((grp * VB >> 4) ^ kv8_swizzle_v<D>(2 * tq + row)) << 4);
-          if constexpr (VW == 4) {
-            const uint4 v = lds16(at);
-            vc[r][0] = v.x;
-            vc[r][1] = v.y;
-            vc[r][2] = v.z;
-            vc[r][3] = v.w;
-          } else {
-            const uint2 v = lds8(at);
-            vc[r][0] = v.x;
-            vc[r][1] = v.y;
-          }
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], sh));
+          rt[e] = fmaxf(rt[e], __shfl_xor_sync(0xffffffffu, rt[e], sh));
         }
+        const float mn = fmaxf(m_run[e], mt[e]), rn = fmaxf(r_run[e], rt[e]);
+        // a head with no token so far has l = 0 and o = 0: any factor serves
+        l_run[e] *= m_run[e] == mn ? 1.f : fast_exp2(m_run[e] - mn);
+        const float al = r_run[e] == rn ? 1.f : fast_exp2(r_run[e] - rn);
+        m_run[e] = mn;
+        r_run[e] = rn;
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // bytes 2h and 2h + 1 of the word: m-tile 2j + h
-            const uint32_t sel = h ? 0x7362 : 0x5140;
-            uint32_t a0, a1, a2, a3;
-            kv8_to_f16<FMT>(__byte_perm(vc[0][j], vc[1][j], sel), a0, a1);
-            kv8_to_f16<FMT>(__byte_perm(vc[2][j], vc[3][j], sel), a2, a3);
-            mma_16816_f16(o[2 * j + h], a0, a1, a2, a3, pb[u][0], pb[u][1]);
-          }
+        for (int j = 0; j < MT; ++j) {
+          o[j][e] *= al;
+          o[j][2 + e] *= al;
         }
       }
     }
-    cp_async_wait<0>();
-    if (!DENSE) __syncthreads();  // the gather list is free for the next sub-chunk
+    // a head with no kept token so far subtracts 0: every exponent is -inf
+    float mu[2], ru[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mu[e] = m_run[e] == kNegInf ? 0.f : m_run[e];
+      ru[e] = r_run[e] == kNegInf ? 0.f : r_run[e] - 7.f;
+      l_run[e] += fast_exp2(x[e] - mu[e]) + fast_exp2(x[2 + e] - mu[e]);
+    }
+    const uint32_t pb0 = movmatrix_trans(pack_f16(fast_exp2(y[0] - ru[0]), fast_exp2(y[1] - ru[1])));
+    const uint32_t pb1 = movmatrix_trans(pack_f16(fast_exp2(y[2] - ru[0]), fast_exp2(y[3] - ru[1])));
+    // ---- O^T += V^T P^T
+    uint32_t vc[4][VW];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = (r & 1) + 8 * (r >> 1);  // + 2tq
+      const uint32_t at = v_src + off + row * D + (((grp * VB >> 4) ^ kv8_swizzle_v<D>(2 * tq + row)) << 4);
+      if constexpr (VW == 4) {
+        const uint4 v = lds16(at);
+        vc[r][0] = v.x;
+        vc[r][1] = v.y;
+        vc[r][2] = v.z;
+        vc[r][3] = v.w;
+      } else {
+        const uint2 v = lds8(at);
+        vc[r][0] = v.x;
+        vc[r][1] = v.y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VW; ++j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // bytes 2h and 2h + 1 of the word: m-tile 2j + h
+        const uint32_t sel = h ? 0x7362 : 0x5140;
+        uint32_t a0, a1, a2, a3;
+        kv8_to_f16<FMT>(__byte_perm(vc[0][j], vc[1][j], sel), a0, a1);
+        kv8_to_f16<FMT>(__byte_perm(vc[2][j], vc[3][j], sel), a2, a3);
+        mma_16816_f16(o[2 * j + h], a0, a1, a2, a3, pb0, pb1);
+      }
+    }
   }
+  cp_async_wait<0>();
 
   // ---- merge the four warps through shared memory (reuses the ring)
   __syncthreads();
