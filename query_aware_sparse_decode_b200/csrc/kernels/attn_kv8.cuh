@@ -192,12 +192,6 @@ __device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
   asm("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p) {
-  uint2 v;
-  asm("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
 // The bf16 queries of a group as fp16 B fragments of S^T = K Q^T.  Lane
 // (grp, tq) of head grp holds dims 64i + 16tq + 4j + {0,1 | 2,3} in
 // fragment 4i + j: the dims of the 16-byte pieces it loads of a K row (the
@@ -237,6 +231,25 @@ __device__ __forceinline__ void load_q_f16(const void* q, size_t head0, int grp,
   qs[1] = kv8_pow2(-__shfl_sync(0xffffffffu, up, (8 * tq + 4) & 31));
 }
 
+// S^T of one tile: ka[i], kb[i] are pieces tq + 4i of rows grp and grp + 8;
+// s[0..1] = row grp, s[2..3] = row grp + 8, heads 2tq + {0,1}, over qs.
+template <int FMT, int D>
+__device__ __forceinline__ void kv8_scores(const uint4 (&ka)[D / 64], const uint4 (&kb)[D / 64],
+                                           const uint32_t (&qb)[D / 16][2], float (&s)[4]) {
+  s[0] = s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const uint32_t wa[4] = {ka[i].x, ka[i].y, ka[i].z, ka[i].w}, wb[4] = {kb[i].x, kb[i].y, kb[i].z, kb[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a0, a1, a2, a3;
+      kv8_to_f16<FMT>(wa[j], a0, a2);
+      kv8_to_f16<FMT>(wb[j], a1, a3);
+      mma_16816_f16(s, a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
+    }
+  }
+}
+
 // Ring of one warp: kKv8Stages tiles of 16 K and V rows.
 constexpr int kKv8Stages = 3;
 constexpr int kKv8Seg = 256;  // tokens of a warp's gather list
@@ -257,6 +270,8 @@ constexpr int attn_kv8_smem() {
 // 16-byte pieces of a cached row are stored at piece ^ swizzle(row), so that the
 // lanes of a shared-memory phase touch different banks: for K two rows' pieces
 // tq, for V rows 0, 2, 4, 6 (+ 1) of two neighbouring pieces.
+// log2 of a V scale; finite or -inf, so that a masked token's weight stays zero over any scale
+__device__ __forceinline__ float kv8_log2_scale(float vs) { return fminf(__log2f(vs), 1e30f); }
 template <int D>
 __device__ __forceinline__ int kv8_swizzle_k(int row) { return D == 128 ? (row & 1) << 2 : 0; }
 template <int D>
@@ -284,7 +299,9 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // are exact in fp16) and fp32 accumulators.  The codes reach the A fragments
 // without ldmatrix or shuffles:
 //  - K: lane (grp, tq) takes 16-byte pieces of rows grp and grp + 8; a word
-//    (4 dims) is one k-step's share of a lane;
+//    (4 dims) is one k-step's share of a lane (fp8 mma.sync would take the codes as they
+//    are, but sm_100a expands it into the same conversions: 557 instructions a tile
+//    instead of 398);
 //  - V: it takes D/8 bytes (dims grp D/8 ..) of token rows 2tq, 2tq+1, 2tq+8,
 //    2tq+9; byte permutes pair the tokens of a dim, and m-tile mt takes dims
 //    grp D/8 + 2mt and + 2mt + 1 as its rows grp and grp + 8.
@@ -301,19 +318,18 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // segment's.  No barrier joins the warps, and the ring does not drain between
 // segments (a CTA-wide list cost 40 % of the stalls).
 //
-// Softmax (log2 domain, fp32): l sums p = 2^(x - m); the weights of the V
-// codes are w = 2^(x + log2 vs - r + 7) with their own running exponent r, so
-// that fp16 holds them whatever the blocks' scales are.  m and r need
-// not be the exact maxima: they are raised only when a logit passes them by
-// 8 (p <= 2^8, w <= 2^15), which after the first tiles is rare, and saves the
-// cross-lane maximum of every tile.  Weights keep fp16's 11 bits down to
-// 2^-21 of the largest one.
+// Softmax (log2 domain, fp32): l sums p = 2^(x - T); the weights of the V codes
+// are w = 2^(x + log2 vs - R + 15) with a reference of their own, so that fp16
+// holds them whatever the blocks' scales are.  T and R are not the exact maxima
+// but 8 above one: they move only when a logit passes them (p <= 1, w <= 2^15),
+// which after the first tiles is rare, and saves the cross-lane maximum of every
+// tile.  Weights keep fp16's 11 bits down to 2^-21 of the largest one.
 template <int FMT, int D, int GS, bool DENSE>
 __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(const AttnKv8Params p) {
   pdl_wait();
   pdl_trigger();
   static_assert(D == 64 || D == 128, "head dim");
-  constexpr int KSTEPS = D / 16, MT = D / 16;
+  constexpr int MT = D / 16;
   constexpr int KLD = D / 64;                   // 16-byte pieces of a K row per lane
   constexpr int VW = D / 32, VB = D / 8;        // words and bytes of a V row per lane
   constexpr int VOFF = kAttnTile * D;           // V rows of a stage
@@ -338,14 +354,13 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   // per stage: DENSE: the block's (ks, vs); else the 16 tokens' (ks log2e/sqrt(D), log2 vs, head bits)
   const uint32_t meta = ring + kKv8Stages * STAGE;
 
-  uint32_t qb[KSTEPS][2];
-  float qs[2];
   const uint32_t head_bits = ((1u << GS) - 1u) >> (2 * tq) & 3u;
   float o[MT][4];  // dims grp D/8 + 2mt (+1), heads 2tq + {0,1}
 #pragma unroll
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float m_run[2] = {kNegInf, kNegInf}, r_run[2] = {kNegInf, kNegInf}, l_run[2] = {0.f, 0.f};
-
+  // of heads 2tq + {0,1}: the reference T (kNone: no token yet), T - R + 15, the lane's part of l
+  constexpr float kNone = -1e30f;
+  float ref[2] = {kNone, kNone}, lift[2] = {15.f, 15.f}, l_run[2] = {0.f, 0.f};
 
   // copies of a tile's 16 rows (of cache rows rows[r] = that of token c_row + CR r)
   auto copy_rows = [&](uint32_t off, const uint32_t (&rows)[kAttnTile / CR]) {
@@ -432,7 +447,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     }
     const float vs = __shfl_sync(0xffffffffu, n_scale, (lane & 15) + 16);
     if (lane < 16)
-      blocks[lane] = make_uint4(n_row, __float_as_uint(n_scale * p.scale_log2), __float_as_uint(__log2f(vs)), 0u);
+      blocks[lane] = make_uint4(n_row, __float_as_uint(n_scale * p.scale_log2), __float_as_uint(kv8_log2_scale(vs)), 0u);
     cnt = (int)__shfl_sync(0xffffffffu, incl, 31);
     pos = 0;
     seg += kKv8Seg;
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
         if (lane == 1) cp_async_4(dst + 4, p.v_scale + (row >> 4));
       } else if (lane == 0) {  // a page outside the pool: the block's scale is NaN
         atomicOr(p.status, TB_DEV_ERR_INDEX);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(0x7fffffff) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(0x7fffffff), "r"(0x3f800000) : "memory");
       }
 #pragma unroll
       for (int r = 0; r < kAttnTile / CR; ++r) rows[r] = row + min(c_row + CR * r, last);
@@ -505,6 +520,8 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     if (issue(s)) ++queued;
     cp_async_commit();
   }
+  uint32_t qb[D / 16][2];
+  float qs[2];
   load_q_f16<D, GS>(p.q, (size_t)b * p.Hq + g * GS, grp, tq, qb, qs);
   for (int it = 0; it < queued; ++it) {
     __syncwarp();  // the stage refilled now has been read by every lane
@@ -514,86 +531,89 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     __syncwarp();  // the pieces come from other lanes
     const uint32_t stage = (uint32_t)(it % kKv8Stages), off = stage * STAGE;
     // ---- S^T = K Q^T: s[0..1] = token grp, s[2..3] = grp + 8; heads 2tq + {0,1}
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float s[4];
+    {
+      uint4 ka[KLD], kb[KLD];  // rows grp, grp + 8
 #pragma unroll
-    for (int i = 0; i < KLD; ++i) {
-      const uint32_t at = k_src + off + (((tq + 4 * i) ^ kv8_swizzle_k<D>(grp)) << 4);
-      const uint4 ka = lds16(at), kb = lds16(at + 8 * D);  // rows grp, grp + 8
-      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t a0, a1, a2, a3;
-        kv8_to_f16<FMT>(wa[j], a0, a2);
-        kv8_to_f16<FMT>(wb[j], a1, a3);
-        mma_16816_f16(s, a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
+      for (int i = 0; i < KLD; ++i) {
+        const uint32_t at = k_src + off + (((tq + 4 * i) ^ kv8_swizzle_k<D>(grp)) << 4);
+        ka[i] = lds16(at);
+        kb[i] = lds16(at + 8 * D);
       }
+      kv8_scores<FMT, D>(ka, kb, qb, s);
     }
-    float2 c[2];     // of tokens grp and grp + 8: ks log2e/sqrt(D), log2 vs
-    uint32_t hb[2];  // their bits of the lane's two heads
+    // x = s f; d = x - T; z = d + log2 vs + T - R + 15
+    float f[2][2], ev[2];
+    uint32_t hb[2];  // tokens grp and grp + 8: bits of the lane's two heads
+    bool masked = true;
     if constexpr (DENSE) {
       const uint2 sc = lds8(meta + stage * (kAttnTile * 16));
       const float ks = __uint_as_float(sc.x);
-      c[0] = c[1] = make_float2(ks * p.scale_log2, __log2f(__uint_as_float(sc.y)));
+      ev[0] = ev[1] = kv8_log2_scale(__uint_as_float(sc.y));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) f[0][e] = f[1][e] = qs[e] * (ks * p.scale_log2);
       const int left = ks == ks ? t1 - t0 - (warp + it * kAttnWarps) * kAttnTile : 0;
-      hb[0] = grp < left ? head_bits : 0u;
-      hb[1] = grp + 8 < left ? head_bits : 0u;
+      masked = left < kAttnTile;
+      hb[0] = grp < left ? 3u : 0u;
+      hb[1] = grp + 8 < left ? 3u : 0u;
     } else {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const uint4 e = lds16(meta + (stage * kAttnTile + grp + 8 * r) * 16);
-        c[r] = make_float2(__uint_as_float(e.x), __uint_as_float(e.y));
+        ev[r] = __uint_as_float(e.y);
+        f[r][0] = qs[0] * __uint_as_float(e.x);
+        f[r][1] = qs[1] * __uint_as_float(e.x);
         hb[r] = e.z >> (2 * tq) & head_bits;
       }
     }
-    float x[4], y[4];
-    float mt[2], rt[2];
+    float d[4], z[4];
+    auto exponents = [&]() {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // a masked token's weight is zero whatever its block's scale says
-        const bool in = hb[r] >> e & 1u;
-        x[2 * r + e] = in ? s[2 * r + e] * qs[e] * c[r].x : kNegInf;
-        y[2 * r + e] = in ? x[2 * r + e] + c[r].y : kNegInf;
-      }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mt[e] = fmaxf(x[e], x[2 + e]);
-      rt[e] = fmaxf(y[e], y[2 + e]);
-    }
-    const bool over = mt[0] > m_run[0] + 8.f || mt[1] > m_run[1] + 8.f || rt[0] > r_run[0] + 8.f ||
-                      rt[1] > r_run[1] + 8.f;
-    if (__any_sync(0xffffffffu, over)) {
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * r + e;
+          d[j] = fmaf(s[j], f[r][e], -ref[e]);
+          if (masked && !(hb[r] >> e & 1u)) d[j] = kNegInf;
+          z[j] = d[j] + (ev[r] + lift[e]);
+        }
+    };
+    exponents();
+    const float dm = fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])), zm = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    if (__any_sync(0xffffffffu, dm > 0.f || zm > 15.f)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        float mt = kNegInf, rt = kNegInf;  // the tile's largest x and x + log2 vs of the head
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (!masked || (hb[r] >> e & 1u)) {
+            mt = fmaxf(mt, s[2 * r + e] * f[r][e]);
+            rt = fmaxf(rt, s[2 * r + e] * f[r][e] + ev[r]);
+          }
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
-          mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], sh));
-          rt[e] = fmaxf(rt[e], __shfl_xor_sync(0xffffffffu, rt[e], sh));
+          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, sh));
+          rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, sh));
         }
-        const float mn = fmaxf(m_run[e], mt[e]), rn = fmaxf(r_run[e], rt[e]);
+        const float t_old = ref[e], r_old = t_old - lift[e] + 15.f;
+        const float t_new = mt > t_old ? mt + 8.f : t_old, r_new = rt > r_old ? rt + 8.f : r_old;
         // a head with no token so far has l = 0 and o = 0: any factor serves
-        l_run[e] *= m_run[e] == mn ? 1.f : fast_exp2(m_run[e] - mn);
-        const float al = r_run[e] == rn ? 1.f : fast_exp2(r_run[e] - rn);
-        m_run[e] = mn;
-        r_run[e] = rn;
+        if (t_new != t_old) l_run[e] *= fast_exp2(t_old - t_new);
+        const float al = r_new != r_old ? fast_exp2(r_old - r_new) : 1.f;
+        ref[e] = t_new;
+        lift[e] = t_new - r_new + 15.f;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
           o[j][e] *= al;
           o[j][2 + e] *= al;
         }
       }
+      exponents();
     }
-    // a head with no kept token so far subtracts 0: every exponent is -inf
-    float mu[2], ru[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mu[e] = m_run[e] == kNegInf ? 0.f : m_run[e];
-      ru[e] = r_run[e] == kNegInf ? 0.f : r_run[e] - 7.f;
-      l_run[e] += fast_exp2(x[e] - mu[e]) + fast_exp2(x[2 + e] - mu[e]);
-    }
-    const uint32_t pb0 = movmatrix_trans(pack_f16(fast_exp2(y[0] - ru[0]), fast_exp2(y[1] - ru[1])));
-    const uint32_t pb1 = movmatrix_trans(pack_f16(fast_exp2(y[2] - ru[0]), fast_exp2(y[3] - ru[1])));
+    for (int e = 0; e < 2; ++e) l_run[e] += fast_exp2(d[e]) + fast_exp2(d[2 + e]);
+    const uint32_t pb0 = movmatrix_trans(pack_f16(fast_exp2(z[0]), fast_exp2(z[1])));
+    const uint32_t pb1 = movmatrix_trans(pack_f16(fast_exp2(z[2]), fast_exp2(z[3])));
     // ---- O^T += V^T P^T
     uint32_t vc[4][VW];
 #pragma unroll
@@ -638,11 +658,10 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     const int h = 2 * tq + e;
     if (h < GS) {
       if (grp == 0) {
-        wm[warp * GS + h] = m_run[e];
+        wm[warp * GS + h] = ref[e] == kNone ? kNegInf : ref[e];
         wl[warp * GS + h] = l_run[e];
       }
-      // back from the weights' exponent to m's
-      const float f = r_run[e] == kNegInf ? 0.f : exp2f(r_run[e] - 7.f - m_run[e]);
+      const float f = exp2f(-lift[e]);  // back from the weights' reference to T
       float* dst = wo + (warp * GS + h) * D + grp * (D / 8);
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
@@ -719,25 +738,14 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
     for (int u = 0; u < AHEAD; ++u) {
       const int tc = tt + u * stride;
       if (tc >= t1) break;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < KLD; ++i) {
-        const uint32_t wa[4] = {kc[u][0][i].x, kc[u][0][i].y, kc[u][0][i].z, kc[u][0][i].w};
-        const uint32_t wb[4] = {kc[u][1][i].x, kc[u][1][i].y, kc[u][1][i].z, kc[u][1][i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t a0, a1, a2, a3;
-          kv8_to_f16<FMT>(wa[j], a0, a2);
-          kv8_to_f16<FMT>(wb[j], a1, a3);
-          mma_16816_f16(s, a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
-        }
-      }
+      float s[4];
+      kv8_scores<FMT, D>(kc[u][0], kc[u][1], qb, s);
       const float sc = ks[u];
       if (tc + AHEAD * stride < t1) load(u, tc + AHEAD * stride);
       const bool in[2] = {tc + grp < t1 && sc == sc, tc + grp + 8 < t1 && sc == sc};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float xa = in[0] ? s[e] * qs[e] * sc : kNegInf, xb = in[1] ? s[2 + e] * qs[e] * sc : kNegInf;
+        const float xa = in[0] ? s[e] * (qs[e] * sc) : kNegInf, xb = in[1] ? s[2 + e] * (qs[e] * sc) : kNegInf;
         if (real[e]) {
           if (tc + grp < t1) lrow[e][tc + grp] = xa;
           if (tc + grp + 8 < t1) lrow[e][tc + grp + 8] = xb;
