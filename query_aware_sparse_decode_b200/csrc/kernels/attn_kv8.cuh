@@ -25,10 +25,11 @@ struct AttnKv8Params : AttnParams {
 // 131072: 203 us in one wave of 7296 tokens, 183 us with 2048; short chunks in
 // several waves lose: B = 16, L = 8192, 66 us either way).
 constexpr int kKv8CtasPerSm = 4;
-constexpr int kKv8MinChunk = 128;
+constexpr int kKv8MinChunk = 128;    // a tile or two a warp; the FMA kernel of fp32 queries takes
+constexpr int kKv8MinChunkF32 = 32;  // its tokens one by one: B = 2, L = 512: 16.4 us with 128, 9.6 us with 32
 constexpr int kKv8LongChunk = 2048;
-inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch, int max_splits, int* chunk_out,
-                           int* nsplit_out) {
+inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch, int max_splits, int min_chunk,
+                           int* chunk_out, int* nsplit_out) {
   long long total = 0;
   int longest = 1;
   for (int b = 0; b < batch; ++b) {
@@ -41,7 +42,7 @@ inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch
   long long chunk = (total * kv_heads + slots - 1) / slots;
   const long long least = (longest + max_splits - 1) / max_splits;
   chunk = chunk < least ? least : chunk;
-  chunk = chunk < kKv8MinChunk ? kKv8MinChunk : (chunk + 31) / 32 * 32;
+  chunk = chunk < min_chunk ? min_chunk : (chunk + 31) / 32 * 32;
   for (;;) {
     long long n = 0, next = longest + 31;  // the CTAs, and the next chunk that has fewer
     for (int b = 0; b < batch; ++b) {
@@ -80,6 +81,19 @@ __device__ __forceinline__ int build_union_list_kv8(const AttnKv8Params& p, int 
   });
 }
 
+__device__ __forceinline__ void load_codes(uint8_t (&c)[4], const uint8_t* p) {
+  const uchar4 v = *reinterpret_cast<const uchar4*>(p);
+  c[0] = v.x;
+  c[1] = v.y;
+  c[2] = v.z;
+  c[3] = v.w;
+}
+__device__ __forceinline__ void load_codes(uint8_t (&c)[2], const uint8_t* p) {
+  const uchar2 v = *reinterpret_cast<const uchar2*>(p);
+  c[0] = v.x;
+  c[1] = v.y;
+}
+
 // fp32 queries, fp32 FMA: one warp per token at a time, lane owns D/32 consecutive dims.
 template <int FMT, int D, int GS>
 __global__ void __launch_bounds__(kAttnThreads) attn_kv8_f32_kernel(const AttnKv8Params p) {
@@ -114,31 +128,38 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kv8_f32_kernel(const AttnKv
   }
   for (int sc0 = t0; sc0 < t1; sc0 += kAttnMaxChunk) {
     const int n = build_union_list_kv8<GS>(p, b, g, sc0, min(sc0 + kAttnMaxChunk, t1), list_idx, list_hb, scan_sm);
-    for (int i = warp; i < n; i += kAttnWarps) {
-      const uint32_t row = (uint32_t)list_idx[i];
-      const uint32_t hb = list_hb[i];
-      const float ks = p.k_scale[row >> 4] * p.scale_log2, vs = p.v_scale[row >> 4];
-      float kv[DPL], vv[DPL];
+    constexpr int AHEAD = 4;  // tokens whose rows and scales are requested together
+    for (int i0 = warp; i0 < n; i0 += AHEAD * kAttnWarps) {
+      uint8_t kc[AHEAD][DPL], vc[AHEAD][DPL];
+      float ks[AHEAD], vs[AHEAD];
 #pragma unroll
-      for (int j = 0; j < DPL; ++j) {
-        kv[j] = kv8_decode<FMT>(Kb[(size_t)row * D + j]);
-        vv[j] = kv8_decode<FMT>(Vb[(size_t)row * D + j]) * vs;
+      for (int u = 0; u < AHEAD; ++u) {
+        const uint32_t row = (uint32_t)list_idx[min(i0 + u * kAttnWarps, n - 1)];
+        load_codes(kc[u], Kb + (size_t)row * D);
+        load_codes(vc[u], Vb + (size_t)row * D);
+        ks[u] = p.k_scale[row >> 4] * p.scale_log2;
+        vs[u] = p.v_scale[row >> 4];
       }
 #pragma unroll
-      for (int hh = 0; hh < GS; ++hh) {
-        if (!((hb >> hh) & 1u)) continue;
-        float dot = 0.f;
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u * kAttnWarps;
+        const uint32_t hb = i < n ? list_hb[i] : 0u;
 #pragma unroll
-        for (int j = 0; j < DPL; ++j) dot = fmaf(q[hh][j], kv[j], dot);
+        for (int hh = 0; hh < GS; ++hh) {
+          if (!((hb >> hh) & 1u)) continue;
+          float dot = 0.f;
 #pragma unroll
-        for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        const float s = dot * ks;
-        const float mn = fmaxf(m[hh], s);
-        const float alpha = exp2f(m[hh] - mn), pw = exp2f(s - mn);
-        l[hh] = l[hh] * alpha + pw;
+          for (int j = 0; j < DPL; ++j) dot = fmaf(q[hh][j], kv8_decode<FMT>(kc[u][j]), dot);
 #pragma unroll
-        for (int j = 0; j < DPL; ++j) o[hh][j] = o[hh][j] * alpha + pw * vv[j];
-        m[hh] = mn;
+          for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+          const float s = dot * ks[u];
+          const float mn = fmaxf(m[hh], s);
+          const float alpha = exp2f(m[hh] - mn), pw = exp2f(s - mn);
+          l[hh] = l[hh] * alpha + pw;
+#pragma unroll
+          for (int j = 0; j < DPL; ++j) o[hh][j] = o[hh][j] * alpha + pw * (kv8_decode<FMT>(vc[u][j]) * vs[u]);
+          m[hh] = mn;
+        }
       }
     }
     __syncthreads();  // the gather list is free for the next sub-chunk

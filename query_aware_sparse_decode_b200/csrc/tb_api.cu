@@ -406,7 +406,9 @@ static tb_status launch_attn_kv8_as(bool bf16, const AttnKv8Params& p, dim3 grid
   auto k = !bf16 ? attn_kv8_f32_kernel<F, D, GS> : dense ? attn_kv8_kernel<F, D, GS, true> : attn_kv8_kernel<F, D, GS, false>;
   const int smem = !bf16 ? attn_kv8_f32_smem<D, GS>()
                          : dense ? attn_kv8_smem<D, GS, true>() : attn_kv8_smem<D, GS, false>();
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return TB_ERR_CUDA;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TB_ERR_CUDA;
   launch_pdl(k, grid, dim3(kAttnThreads), smem, st, p);
   return cuda_status(cudaGetLastError());
 }
@@ -453,7 +455,8 @@ static tb_status launch_attn(tb_ctx* ctx, int layer, const void* q, const uint32
   for (int b = 0; b < c.batch; ++b) p.lens[b] = ls.lens[b];
   int chunk = 0;
   if (ls.kv8)
-    attn_split_kv8(ctx->num_sms, c.n_kv_heads, ls.lens, c.batch, ctx->lay.max_splits, &chunk, &p.nsplit);
+    attn_split_kv8(ctx->num_sms, c.n_kv_heads, ls.lens, c.batch, ctx->lay.max_splits,
+                   c.kv_dtype == TB_BF16 ? kKv8MinChunk : kKv8MinChunkF32, &chunk, &p.nsplit);
   else if (!attn_split(ctx->num_sms, c.batch * c.n_kv_heads, maxL, &chunk, &p.nsplit))
     return TB_ERR_UNSUPPORTED;
   p.chunk = chunk;

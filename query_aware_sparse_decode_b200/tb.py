@@ -122,20 +122,20 @@ def _check(status: int, what: str) -> None:
         raise TBError(status, what)
 
 
-def _ptr(t: torch.Tensor | None):
+def _ptr(t: torch.Tensor | None) -> int | None:
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(stream) -> int:
+    if stream is None:  # the current stream's handle, without the Python stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def make_config(n_layers, batch, n_q_heads, n_kv_heads, head_dim, d_imp, producer_freq, max_len, kv_dtype,
@@ -156,6 +156,17 @@ def kimp_cache(cfg: Config, device="cuda", fill=0.0) -> torch.Tensor:
     (256-token tiles, dimension-major inside), fp32 or bf16 as cfg says."""
     dt = torch.bfloat16 if cfg.kimp_bf16 else torch.float32
     return torch.full((cfg.batch, cfg.n_kv_heads, cfg.max_len // 256, cfg.d_imp, 256), fill, dtype=dt, device=device)
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _row_strides(name: str, t: torch.Tensor):
+    """(batch, head, token) strides of a [B][Hkv][n][D] tensor; those of single entries are not used."""
+    s, n = t.stride(), t.shape
+    if s[3] != 1:
+        raise ValueError(f"{name}: a row's elements must be contiguous")
+    return _Strides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
 
 
 KV8_FORMATS = {"e4m3": (TB_KV8_E4M3, torch.float8_e4m3fn), "int8": (TB_KV8_INT8, torch.int8)}
@@ -204,6 +215,10 @@ class Context:
                "tb_init")
         self._h = h
         self._keep = {}  # tensors bound to layers stay alive with the context
+        self._index = self.workspace.get_device()
+        self._kv_dtype = torch.bfloat16 if cfg.kv_dtype == TB_BF16 else torch.float32
+        self._rows = (cfg.batch, cfg.n_kv_heads, cfg.head_dim)
+        self._lens_type = ctypes.c_int32 * cfg.batch
 
     # -------------------------------------------------------------- setup
     def _kimp_type_ok(self, kimp_cache) -> None:
@@ -218,7 +233,7 @@ class Context:
         self._keep[layer] = (k_cache, v_cache, kimp_cache, w_k)
 
     def set_seq_lens(self, layer: int, lens) -> None:
-        arr = (ctypes.c_int32 * self.cfg.batch)(*[int(x) for x in lens])
+        arr = self._lens_type(*[int(x) for x in lens])
         _check(lib().tb_set_seq_lens(self._h, layer, arr), "tb_set_seq_lens")
 
     def seq_lens(self, layer: int) -> list:
@@ -295,16 +310,18 @@ class Context:
     def _expect(self, name, t, shape, dtype) -> None:
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the context on {self.device}")
+        if t.get_device() != self._index:
+            raise ValueError(f"{name} is on {t.device}, the context on cuda:{self._index}")
 
-    def _kv_torch_dtype(self):
-        return torch.bfloat16 if self.cfg.kv_dtype == TB_BF16 else torch.float32
-
-    def _own_stream(self, stream) -> ctypes.c_void_p:
-        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+    def _on_device(self, call, what: str, stream) -> None:
+        """call(stream handle) with the context's device current."""
+        if torch._C._cuda_getDevice() == self._index:
+            _check(call(_stream(stream)), what)
+        else:
+            with torch.cuda.device(self._index):
+                _check(call(_stream(stream)), what)
 
     def _check_kv8(self, lead, rows, k, v, k_scale, v_scale, kimp_cache, w_k) -> int:
         c = self.cfg
@@ -318,7 +335,7 @@ class Context:
         self._kimp_type_ok(kimp_cache)
         self._expect("K_imp cache", kimp_cache, (c.batch, c.n_kv_heads, c.max_len // 256, c.d_imp, 256),
                      kimp_cache.dtype)
-        self._expect("w_k", w_k, (c.head_dim, c.d_imp), self._kv_torch_dtype())
+        self._expect("w_k", w_k, (c.head_dim, c.d_imp), self._kv_dtype)
         return fmt
 
     def bind_layer_kv8(self, layer: int, k_codes, v_codes, k_scale, v_scale, kimp_cache, w_k) -> None:
@@ -346,37 +363,35 @@ class Context:
         sequence of an 8-bit layer, and forms their K_imp.  k, v:
         [B][Hkv][n][D] (kv_dtype), any strides with contiguous rows (a view
         of a fused projection's output serves); counts: n for all by default."""
-        c = self.cfg
+        B, H, D = self._rows
         if k.dim() != 4 or k.shape != v.shape:
             raise ValueError(f"k and v must be [B][Hkv][n][D] alike, got {tuple(k.shape)} and {tuple(v.shape)}")
         n = k.shape[2]
-        for name, t in (("k", k), ("v", v)):
-            self._expect(name, t, (c.batch, c.n_kv_heads, n, c.head_dim), self._kv_torch_dtype())
-            if t.stride(3) != 1:
-                raise ValueError(f"{name}: a row's elements must be contiguous")
-        counts = [n] * c.batch if counts is None else [int(x) for x in counts]
-        if len(counts) != c.batch or any(x < 0 or x > n for x in counts):
-            raise ValueError(f"counts must be {c.batch} numbers in [0, {n}], got {counts}")
+        self._expect("k", k, (B, H, n, D), self._kv_dtype)
+        self._expect("v", v, (B, H, n, D), self._kv_dtype)
+        counts = [n] * B if counts is None else [int(x) for x in counts]
+        if len(counts) != B or min(counts) < 0 or max(counts) > n:
+            raise ValueError(f"counts must be {B} numbers in [0, {n}], got {counts}")
         if n == 0:
             return
-        strides = [(ctypes.c_int64 * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))) for t in (k, v)]
-        with torch.cuda.device(self.device):
-            _check(lib().tb_append_kv_rows(self._h, layer, ctypes.c_void_p(k.data_ptr()),
-                                           ctypes.c_void_p(v.data_ptr()), strides[0], strides[1],
-                                           (ctypes.c_int32 * c.batch)(*counts), self._own_stream(stream)),
-                   "tb_append_kv_rows")
+        ks, vs = _row_strides("k", k), _row_strides("v", v)
+        arr = self._lens_type(*counts)
+        self._on_device(lambda st: lib().tb_append_kv_rows(self._h, layer, k.data_ptr(), v.data_ptr(), ks, vs, arr, st),
+                        "tb_append_kv_rows", stream)
 
     def read_kv(self, layer: int, start: int, count: int, k_out=None, v_out=None, stream=None) -> None:
         """Rows [start, start + count) of an 8-bit layer as values into k_out
         and/or v_out [B][Hkv][count][D] (kv_dtype); rows past a sequence's
         length are left as they are."""
-        c = self.cfg
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            if t is not None:
-                self._expect(name, t, (c.batch, c.n_kv_heads, count, c.head_dim), self._kv_torch_dtype())
-        with torch.cuda.device(self.device):
-            _check(lib().tb_read_kv(self._h, layer, start, count, _ptr(k_out), _ptr(v_out), self._own_stream(stream)),
-                   "tb_read_kv")
+        B, H, D = self._rows
+        if k_out is not None:
+            self._expect("k_out", k_out, (B, H, count, D), self._kv_dtype)
+        if v_out is not None:
+            self._expect("v_out", v_out, (B, H, count, D), self._kv_dtype)
+        if count == 0 and not (k_out is None and v_out is None):
+            return
+        ko, vo = _ptr(k_out), _ptr(v_out)
+        self._on_device(lambda st: lib().tb_read_kv(self._h, layer, start, count, ko, vo, st), "tb_read_kv", stream)
 
     def selection_cache(self, layer: int):
         """Allocate (zero-filled) and bind layer `layer`'s selection cache;
