@@ -207,12 +207,6 @@ __device__ __forceinline__ void kv8_to_f16(uint32_t w, uint32_t& lo, uint32_t& h
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(c), "r"(0x64806480u));
   }
 }
-// cache codes: read once, straight from L2 into registers
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
-  uint4 v;
-  asm("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
 // The bf16 queries of a group as fp16 B fragments of S^T = K Q^T.  Lane
 // (grp, tq) of head grp holds dims 64i + 16tq + 4j + {0,1 | 2,3} in
 // fragment 4i + j: the dims of the 16-byte pieces it loads of a K row (the
@@ -257,6 +251,7 @@ __device__ __forceinline__ void load_q_f16(const void* q, size_t head0, int grp,
 template <int FMT, int D>
 __device__ __forceinline__ void kv8_scores(const uint4 (&ka)[D / 64], const uint4 (&kb)[D / 64],
                                            const uint32_t (&qb)[D / 16][2], float (&s)[4]) {
+  float s1[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products: each waits 20 cycles for its last
   s[0] = s[1] = s[2] = s[3] = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
@@ -266,9 +261,11 @@ __device__ __forceinline__ void kv8_scores(const uint4 (&ka)[D / 64], const uint
       uint32_t a0, a1, a2, a3;
       kv8_to_f16<FMT>(wa[j], a0, a2);
       kv8_to_f16<FMT>(wb[j], a1, a3);
-      mma_16816_f16(s, a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
+      mma_16816_f16(j & 1 ? s1 : s, a0, a1, a2, a3, qb[4 * i + j][0], qb[4 * i + j][1]);
     }
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s[j] += s1[j];
 }
 
 // Ring of one warp: kKv8Stages tiles of 16 K and V rows.
@@ -703,15 +700,16 @@ struct VoteKv8Params : VoteParams {
 // Soft-vote logits (log2 domain) and per-chunk (max, sum) pairs over 8-bit
 // keys; softvote_reduce_kernel follows.  S^T = K Q^T as in attn_kv8_kernel, over
 // consecutive tokens: a tile of 16 is one block of the cache, so it has one
-// scale and one row lookup.  A warp keeps the next kVoteKv8Ahead tiles' codes
-// in flight in registers.
-constexpr int kVoteKv8Ahead = 2;
+// scale and one row lookup.  A ring of kVoteKv8Stages tiles per warp.
+constexpr int kVoteKv8Stages = 3;
+template <int D>
+constexpr int vote_kv8_smem() { return kVoteWarps * kVoteKv8Stages * (kAttnTile * D + 16); }
 template <int FMT, int D, int GS>
 __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(const VoteKv8Params p) {
   pdl_wait();
   pdl_trigger();
-  constexpr int KLD = D / 64;
-  constexpr int AHEAD = kVoteKv8Ahead;
+  constexpr int KLD = D / 64, NPC = D / 16, CR = 32 / NPC, STAGE = kAttnTile * D;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float wm[kVoteWarps * GS], wl[kVoteWarps * GS];
   const int chunk = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int L = p.lens[b];
@@ -720,65 +718,96 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
   const int t1 = min(t0 + p.chunk, L);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = lane >> 2, tq = lane & 3;
-  const uint8_t* Kb = reinterpret_cast<const uint8_t*>(p.k_cache) + 16 * tq;
+  const int c_row = lane / NPC, c_part = lane % NPC;
+  const uint8_t* Kb = reinterpret_cast<const uint8_t*>(p.k_cache) + 16 * c_part;
+  const uint32_t ring = smem_u32(smem) + warp * kVoteKv8Stages * STAGE;
+  const uint32_t scales = smem_u32(smem) + kVoteWarps * kVoteKv8Stages * STAGE + warp * kVoteKv8Stages * 16;
+  const int my_n = (t1 - t0 - warp * kAttnTile + kVoteWarps * kAttnTile - 1) / (kVoteWarps * kAttnTile);  // may be <= 0
+  auto issue = [&](int it) {
+    const int tt = t0 + (warp + it * kVoteWarps) * kAttnTile;
+    const uint32_t stage = (uint32_t)(it % kVoteKv8Stages);
+    uint32_t row;
+    const bool ok = kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, tt, &row);
+    const int last = ok ? t1 - 1 - tt : 0;  // rows past the end repeat the last one
+    if (lane == 0) {
+      if (ok) {
+        cp_async_4(scales + 16 * stage, p.k_scale + (row >> 4));
+      } else {  // a page outside the pool: the block's scale is NaN
+        atomicOr(p.status, TB_DEV_ERR_INDEX);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(scales + 16 * stage), "r"(0x7fffffff) : "memory");
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kAttnTile / CR; ++r) {
+      const int rr = c_row + CR * r;
+      cp_async_16u(ring + stage * STAGE + rr * D + ((c_part ^ kv8_swizzle_k<D>(rr)) << 4),
+                   Kb + (size_t)(row + min(rr, last)) * D);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kVoteKv8Stages - 1; ++s) {
+    if (s < my_n) issue(s);
+    cp_async_commit();
+  }
   uint32_t qb[D / 16][2];
   float qs[2];
   load_q_f16<D, GS>(p.q, (size_t)b * p.Hq + g * GS, grp, tq, qb, qs);
   const int hp = 2 * tq;
   const bool real[2] = {hp < GS, hp + 1 < GS};
-  float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // over the lane's tokens
+  // per lane and head: a reference (8 above a logit that passed the last one) and the sum of 2^(x - it)
+  float m[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f};
   float* lrow[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
-    lrow[e] = p.logits + ((size_t)b * p.Hq + g * GS + (real[e] ? hp + e : 0)) * p.max_len;
-
-  uint4 kc[AHEAD][2][KLD];
-  float ks[AHEAD];
-  // tile tt: rows of one block; rows past the chunk's end repeat its last one; a
-  // page outside the pool leaves scale NaN, which marks the tile
-  auto load = [&](int slot, int tt) {
-    uint32_t row;
-    const bool ok = kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, tt, &row);
-    if (!ok && lane == 0) atomicOr(p.status, TB_DEV_ERR_INDEX);
-    const int last = ok ? t1 - 1 - tt : 0;
+    lrow[e] = p.logits + ((size_t)b * p.Hq + g * GS + (real[e] ? hp + e : 0)) * p.max_len + t0 + warp * kAttnTile + grp;
+  for (int it = 0; it < my_n; ++it) {
+    __syncwarp();  // the stage refilled now has been read by every lane
+    if (it + kVoteKv8Stages - 1 < my_n) issue(it + kVoteKv8Stages - 1);
+    cp_async_commit();
+    cp_async_wait<kVoteKv8Stages - 1>();
+    __syncwarp();  // the pieces come from other lanes
+    const uint32_t stage = (uint32_t)(it % kVoteKv8Stages);
+    uint4 ka[KLD], kb[KLD];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint8_t* src = Kb + (size_t)(row + min(grp + 8 * r, last)) * D;
-#pragma unroll
-      for (int i = 0; i < KLD; ++i) kc[slot][r][i] = ld_codes16(src + 64 * i);
+    for (int i = 0; i < KLD; ++i) {
+      const uint32_t at = ring + stage * STAGE + grp * D + (((tq + 4 * i) ^ kv8_swizzle_k<D>(grp)) << 4);
+      ka[i] = lds16(at);
+      kb[i] = lds16(at + 8 * D);
     }
-    ks[slot] = ok ? p.k_scale[row >> 4] * p.scale_log2 : __int_as_float(0x7fffffff);
-  };
-  const int stride = kVoteWarps * kAttnTile;
-  int tt = t0 + warp * kAttnTile;
+    float s[4];
+    kv8_scores<FMT, D>(ka, kb, qb, s);
+    const float ks = __uint_as_float(lds8(scales + 16 * stage).x);
+    const int left = t1 - t0 - (warp + it * kVoteWarps) * kAttnTile;
+    float x[4];
 #pragma unroll
-  for (int u = 0; u < AHEAD; ++u)
-    if (tt + u * stride < t1) load(u, tt + u * stride);
-  for (; tt < t1; tt += AHEAD * stride) {
+    for (int e = 0; e < 2; ++e) {
+      const float f = qs[e] * (ks * p.scale_log2);
+      x[e] = s[e] * f;
+      x[2 + e] = s[2 + e] * f;
+    }
+    const bool in[2] = {grp < left, grp + 8 < left};
+    if (left < kAttnTile || !(ks == ks)) {
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int tc = tt + u * stride;
-      if (tc >= t1) break;
-      float s[4];
-      kv8_scores<FMT, D>(kc[u][0], kc[u][1], qb, s);
-      const float sc = ks[u];
-      if (tc + AHEAD * stride < t1) load(u, tc + AHEAD * stride);
-      const bool in[2] = {tc + grp < t1 && sc == sc, tc + grp + 8 < t1 && sc == sc};
+      for (int j = 0; j < 4; ++j)
+        if (!in[j >> 1] || !(ks == ks)) x[j] = kNegInf;
+    }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float xa = in[0] ? s[e] * (qs[e] * sc) : kNegInf, xb = in[1] ? s[2 + e] * (qs[e] * sc) : kNegInf;
-        if (real[e]) {
-          if (tc + grp < t1) lrow[e][tc + grp] = xa;
-          if (tc + grp + 8 < t1) lrow[e][tc + grp + 8] = xb;
-        }
-        const float mn = fmaxf(m[e], fmaxf(xa, xb));
-        if (mn != kNegInf) {
-          l[e] = l[e] * fast_exp2(m[e] - mn) + fast_exp2(xa - mn) + fast_exp2(xb - mn);
-          m[e] = mn;
-        }
+    for (int e = 0; e < 2; ++e) {
+      if (real[e] && in[0]) lrow[e][0] = x[e];
+      if (real[e] && in[1]) lrow[e][8] = x[2 + e];
+      lrow[e] += kVoteWarps * kAttnTile;
+      const float top = fmaxf(x[e], x[2 + e]);
+      if (top > m[e]) {
+        l[e] *= fast_exp2(m[e] - (top + 8.f));
+        m[e] = top + 8.f;
       }
+      l[e] += fast_exp2(x[e] - m[e]) + fast_exp2(x[2 + e] - m[e]);
     }
   }
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (m[e] == -1e30f) m[e] = kNegInf;  // no token
+  cp_async_wait<0>();
   // merge the lanes' pairs of each head (the 8 lanes with the same tq)
 #pragma unroll
   for (int e = 0; e < 2; ++e) {

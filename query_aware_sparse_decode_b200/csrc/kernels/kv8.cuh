@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kKv8WriteThreads) kv8_write_f32_kernel(const K
 // 2i + h are dims 32i + 8tq + 4h + {0,1 | 2,3}), the input of the block's amax
 // (one warp maximum) and of the codes, stored 8 bytes a lane in whole
 // 32-byte sectors.  W_K's B fragments are staged once per CTA, in lane order.
-// A warp's blocks are gridDim.x apart, so few blocks spread over the CTAs.
+// A warp's blocks are gridDim.x apart, so few blocks spread over the CTAs; the next
+// block's V is requested when V's registers are free, its K when K's are.
 struct Kv8WriteBf16Params : Kv8WriteParams {
   int first[kMaxBatch + 1];  // units (block, head) before sequence b's; [B]: all of them
   int batch;
@@ -231,6 +232,114 @@ __device__ __forceinline__ uint32_t kv8_encode4_any(float x0, float x1, float x2
          (uint32_t)kv8_encode<FMT>(x2 * inv) << 16 | (uint32_t)kv8_encode<FMT>(x3 * inv) << 24;
 }
 
+// A unit of the write: one block of one (b, g).
+struct Kv8Unit {
+  int b, g, t_lo, r0, r1;  // its first token, and the block's new rows [r0, r1)
+  uint32_t row0;           // its first cache row
+  bool ok;                 // false: no page of the pool
+};
+__device__ __forceinline__ Kv8Unit kv8_unit(const Kv8WriteBf16Params& p, int u) {
+  Kv8Unit r;
+  r.b = 0;
+  for (int hi = p.batch; hi - r.b > 1;) {
+    const int mid = (r.b + hi) >> 1;
+    if (p.first[mid] <= u) r.b = mid;
+    else hi = mid;
+  }
+  const int pos = p.pos[r.b], end = pos + p.cnt[r.b];
+  const int per_head = (p.first[r.b + 1] - p.first[r.b]) / p.Hkv;
+  r.g = (u - p.first[r.b]) / per_head;
+  r.t_lo = (pos / kKv8Block + (u - p.first[r.b]) % per_head) * kKv8Block;
+  r.r0 = max(pos - r.t_lo, 0);
+  r.r1 = min(end - r.t_lo, kKv8Block);
+  r.ok = kv_row_checked(p.kl, r.b, r.g, p.Hkv, p.max_len, r.t_lo, &r.row0);
+  return r;
+}
+// The lane's pieces of the unit's new rows (zeros in the others) and the block's old scale.
+template <int D>
+__device__ __forceinline__ void kv8_load_rows(const Kv8WriteBf16Params& p, int kv, const Kv8Unit& u, int grp, int tq,
+                                              uint4 (&x)[2][D / 32], float& old) {
+  const uint16_t* src = reinterpret_cast<const uint16_t*>(p.src[kv]) + u.b * p.sb[kv] + u.g * p.sh[kv] +
+                        (long long)(u.t_lo - p.pos[u.b]) * p.st[kv] + 8 * tq;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = grp + 8 * h;
+    const bool fresh = r >= u.r0 && r < u.r1;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      x[h][i] = fresh ? __ldcs(reinterpret_cast<const uint4*>(src + r * p.st[kv] + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  old = u.r0 > 0 ? p.scale[kv][u.row0 >> 4] : 0.f;
+}
+// Codes and scale of the unit's rows of one tensor.
+template <int FMT, int D>
+__device__ __forceinline__ void kv8_store_rows(const Kv8WriteBf16Params& p, int kv, const Kv8Unit& u, int lane,
+                                               const uint4 (&x)[2][D / 32], float old) {
+  constexpr int NP = D / 32;
+  const int grp = lane >> 2, tq = lane & 3;
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint4 w = x[h][i];
+      m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, w.x), w.y), w.z), w.w);
+    }
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+  const bool odd = top >= 0x7F80u;  // an infinity or a NaN
+  if (odd) {
+    float a = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint32_t w[4] = {x[h][i].x, x[h][i].y, x[h][i].z, x[h][i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a = fmaxf(a, fmaxf(kv8_mag(bf16_lo(w[j])), kv8_mag(bf16_hi(w[j]))));
+      }
+    top = __reduce_max_sync(0xffffffffu, __float_as_uint(a) >> 16);
+    if (lane == 0) atomicOr(p.status, TB_DEV_ERR_VALUE);
+  }
+  float sc = kv8_pow2(kv8_exponent<FMT>(__uint_as_float(top << 16)));
+  float ratio = 1.f;  // of the old scale to the new one, for the block's older rows
+  if (u.r0 > 0) {
+    if (old >= sc) sc = old;
+    else ratio = old * (1.f / sc);
+  }
+  const float inv = 1.f / sc;
+  uint8_t* dst = p.codes[kv] + (size_t)u.row0 * D + 8 * tq;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = grp + 8 * h;
+    if (r >= u.r0 && r < u.r1) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint4 w = x[h][i];
+        uint2 c;
+        if (!odd) {
+          c.x = kv8_encode4<FMT>(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), inv);
+          c.y = kv8_encode4<FMT>(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w), inv);
+        } else {
+          c.x = kv8_encode4_any<FMT>(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), inv);
+          c.y = kv8_encode4_any<FMT>(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w), inv);
+        }
+        *reinterpret_cast<uint2*>(dst + r * D + 32 * i) = c;
+      }
+    } else if (r < u.r0 && ratio != 1.f) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        uint2* at = reinterpret_cast<uint2*>(dst + r * D + 32 * i);
+        float y[4], z[4];
+        kv8_decode4<FMT>(at->x, y);
+        kv8_decode4<FMT>(at->y, z);
+        *at = make_uint2(kv8_encode4_any<FMT>(y[0], y[1], y[2], y[3], ratio),
+                         kv8_encode4_any<FMT>(z[0], z[1], z[2], z[3], ratio));
+      }
+    }
+  }
+  if (lane == 0) p.scale[kv][u.row0 >> 4] = sc;
+}
+
 template <int FMT, int D, int DIMP>
 __global__ void __launch_bounds__(kKv8WriteThreads, 4) kv8_write_bf16_kernel(const Kv8WriteBf16Params p) {
   pdl_wait();
@@ -239,6 +348,16 @@ __global__ void __launch_bounds__(kKv8WriteThreads, 4) kv8_write_bf16_kernel(con
   __shared__ uint2 wf[KST * NT * 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = lane >> 2, tq = lane & 3;
+  const int units = p.first[p.batch], step = gridDim.x * (kKv8WriteThreads / 32);
+  int u = blockIdx.x + warp * gridDim.x;
+  Kv8Unit cur{};
+  uint4 xk[2][NP], xv[2][NP];
+  float old_k = 0.f, old_v = 0.f;
+  if (u < units) {  // the first unit's rows are on their way while W_K is staged
+    cur = kv8_unit(p, u);
+    kv8_load_rows<D>(p, 1, cur, grp, tq, xv, old_v);
+    kv8_load_rows<D>(p, 0, cur, grp, tq, xk, old_k);
+  }
   {
     const uint16_t* W = reinterpret_cast<const uint16_t*>(p.w_k);
 #pragma unroll
@@ -249,131 +368,43 @@ __global__ void __launch_bounds__(kKv8WriteThreads, 4) kv8_write_bf16_kernel(con
     }
   }
   __syncthreads();
-  const int units = p.first[p.batch];
-  for (int u = blockIdx.x + warp * gridDim.x; u < units; u += gridDim.x * (kKv8WriteThreads / 32)) {
-    int b = 0;
-    for (int hi = p.batch; hi - b > 1;) {
-      const int mid = (b + hi) >> 1;
-      if (p.first[mid] <= u) b = mid;
-      else hi = mid;
-    }
-    const int pos = p.pos[b], end = pos + p.cnt[b];
-    const int per_head = (p.first[b + 1] - p.first[b]) / p.Hkv;
-    const int g = (u - p.first[b]) / per_head;
-    const int t_lo = (pos / kKv8Block + (u - p.first[b]) % per_head) * kKv8Block;
-    const int r0 = max(pos - t_lo, 0), r1 = min(end - t_lo, kKv8Block);
-    uint32_t row0;
-    if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t_lo, &row0)) {
-      if (lane == 0) atomicOr(p.status, TB_DEV_ERR_INDEX);
-      continue;
-    }
-    uint4 x[2][2][NP];  // [K, V][row grp, row grp + 8][piece]
+  while (u < units) {
+    u += step;
+    Kv8Unit next{};
+    if (u < units) next = kv8_unit(p, u);
+    if (!cur.ok && lane == 0) atomicOr(p.status, TB_DEV_ERR_INDEX);
+    if (cur.ok) kv8_store_rows<FMT, D>(p, 1, cur, lane, xv, old_v);
+    if (u < units) kv8_load_rows<D>(p, 1, next, grp, tq, xv, old_v);
+    if (cur.ok) {
+      kv8_store_rows<FMT, D>(p, 0, cur, lane, xk, old_k);
+      float acc[NT][4];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(p.src[kv]) + b * p.sb[kv] + g * p.sh[kv] +
-                            (long long)(t_lo - pos) * p.st[kv] + 8 * tq;
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint4 w0 = xk[0][i], w1 = xk[1][i];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 f0 = wf[(2 * i * NT + nt) * 32 + lane], f1 = wf[((2 * i + 1) * NT + nt) * 32 + lane];
+          mma_16816(acc[nt], w0.x, w1.x, w0.y, w1.y, f0.x, f0.y);
+          mma_16816(acc[nt], w0.z, w1.z, w0.w, w1.w, f1.x, f1.y);
+        }
+      }
+      const size_t slab = (size_t)cur.b * p.Hkv + cur.g;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = grp + 8 * h;
-        const bool fresh = r >= r0 && r < r1;
+        if (r < cur.r0 || r >= cur.r1) continue;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          x[kv][h][i] = fresh ? __ldcs(reinterpret_cast<const uint4*>(src + r * p.st[kv] + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            store_kimp(p.kimp, kimp_index(slab, 8 * nt + 2 * tq + e, cur.t_lo + r, DIMP, p.max_len), acc[nt][2 * h + e],
+                       p.kimp_bf16);
       }
     }
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      uint32_t m2 = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const uint4 w = x[kv][h][i];
-          m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, w.x), w.y), w.z), w.w);
-        }
-      uint32_t top = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
-      const bool odd = top >= 0x7F80u;  // an infinity or a NaN
-      if (odd) {
-        float a = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const uint32_t w[4] = {x[kv][h][i].x, x[kv][h][i].y, x[kv][h][i].z, x[kv][h][i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a = fmaxf(a, fmaxf(kv8_mag(bf16_lo(w[j])), kv8_mag(bf16_hi(w[j]))));
-          }
-        top = __reduce_max_sync(0xffffffffu, __float_as_uint(a) >> 16);
-        if (lane == 0) atomicOr(p.status, TB_DEV_ERR_VALUE);
-      }
-      float sc = kv8_pow2(kv8_exponent<FMT>(__uint_as_float(top << 16)));
-      float ratio = 1.f;  // of the old scale to the new one, for the block's older rows
-      if (r0 > 0) {
-        const float old = p.scale[kv][row0 >> 4];
-        if (old >= sc) sc = old;
-        else ratio = old * (1.f / sc);
-      }
-      const float inv = 1.f / sc;
-      uint8_t* dst = p.codes[kv] + (size_t)row0 * D + 8 * tq;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = grp + 8 * h;
-        if (r >= r0 && r < r1) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const uint4 w = x[kv][h][i];
-            uint2 c;
-            if (!odd) {
-              c.x = kv8_encode4<FMT>(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), inv);
-              c.y = kv8_encode4<FMT>(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w), inv);
-            } else {
-              c.x = kv8_encode4_any<FMT>(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), inv);
-              c.y = kv8_encode4_any<FMT>(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w), inv);
-            }
-            *reinterpret_cast<uint2*>(dst + r * D + 32 * i) = c;
-          }
-        } else if (r < r0 && ratio != 1.f) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            uint2* at = reinterpret_cast<uint2*>(dst + r * D + 32 * i);
-            float y[4], z[4];
-            kv8_decode4<FMT>(at->x, y);
-            kv8_decode4<FMT>(at->y, z);
-            *at = make_uint2(kv8_encode4_any<FMT>(y[0], y[1], y[2], y[3], ratio),
-                             kv8_encode4_any<FMT>(z[0], z[1], z[2], z[3], ratio));
-          }
-        }
-      }
-      __syncwarp();  // every lane has read the old scale
-      if (lane == 0) p.scale[kv][row0 >> 4] = sc;
-      if (kv == 0) {
-        float acc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const uint4 w0 = x[0][0][i], w1 = x[0][1][i];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 f0 = wf[(2 * i * NT + nt) * 32 + lane], f1 = wf[((2 * i + 1) * NT + nt) * 32 + lane];
-            mma_16816(acc[nt], w0.x, w1.x, w0.y, w1.y, f0.x, f0.y);
-            mma_16816(acc[nt], w0.z, w1.z, w0.w, w1.w, f1.x, f1.y);
-          }
-        }
-        const size_t slab = (size_t)b * p.Hkv + g;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = grp + 8 * h;
-          if (r < r0 || r >= r1) continue;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              store_kimp(p.kimp, kimp_index(slab, 8 * nt + 2 * tq + e, t_lo + r, DIMP, p.max_len), acc[nt][2 * h + e],
-                         p.kimp_bf16);
-        }
-      }
-    }
+    if (u < units) kv8_load_rows<D>(p, 0, next, grp, tq, xk, old_k);
+    cur = next;
   }
 }
 

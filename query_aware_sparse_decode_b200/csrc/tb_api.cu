@@ -556,7 +556,7 @@ static tb_status launch_softvote(tb_ctx* ctx, int layer, const void* q, float* v
   p8.status = ctx->status;
 #define TB_VOTE8_CASE(F, DV, GSV)                                                             \
   if (ls.kv8 == F && c.head_dim == DV && gs == GSV)                                           \
-    launch_pdl(softvote_kv8_logits_kernel<F, DV, GSV>, grid, dim3(kVoteThreads), 0, st, p8);  \
+    launch_pdl(softvote_kv8_logits_kernel<F, DV, GSV>, grid, dim3(kVoteThreads), vote_kv8_smem<DV>(), st, p8); \
   else
 #define TB_VOTE8_CASES(F)                                                                                   \
   TB_VOTE8_CASE(F, 128, 4) TB_VOTE8_CASE(F, 128, 2) TB_VOTE8_CASE(F, 128, 1) TB_VOTE8_CASE(F, 128, 8)   \
