@@ -165,7 +165,8 @@ TB_API tb_status tb_bind_layer_paged(tb_ctx* ctx, int layer, void* k_pool, void*
  * attention and the soft votes read.  One fp32 scale serves an aligned block
  * of TB_KV8_BLOCK tokens of one (sequence, KV head), for K and for V:
  *
- *   scale = 2^e, e = max(-100, smallest integer with amax <= F 2^e)
+ *   scale = 2^e, e the smallest integer with amax <= F 2^e, at least -100 and
+ *           at most 119 (int8: 121; magnitudes above F 2^e are stored as it)
  *   code  = x / scale rounded to nearest, ties to even
  *
  * with amax the largest finite magnitude of the block's rows and F the
@@ -177,7 +178,7 @@ TB_API tb_status tb_bind_layer_paged(tb_ctx* ctx, int layer, void* k_pool, void*
  * grew; tb_set_seq_lens back into a block keeps its scale.  An infinity is
  * stored as the largest value of its block, a NaN as zero; either sets
  * TB_DEV_ERR_VALUE.  The e4m3 codes 0x7F and 0xFF (NaN) are never written and
- * must not be put there.
+ * must not be put there, nor a scale that is not a positive finite number.
  *   k_codes, v_codes   [B][Hkv][max_len][D]               1 byte
  *   k_scale, v_scale   [B][Hkv][max_len/TB_KV8_BLOCK]     fp32
  * New rows, queries, outputs and W_K keep kv_dtype.  Rows are written by
@@ -217,7 +218,8 @@ TB_API tb_status tb_append_kv_rows(tb_ctx* ctx, int layer, const void* k, const 
 
 /* Reads rows [start, start + count) of every (b, KV head) of an 8-bit layer
  * back as code * scale: k_out, v_out [B][Hkv][count][D] kv_dtype (either may
- * be NULL, not both; exact in bf16 and fp32).  Rows t >= len[b] are left untouched. */
+ * be NULL, not both; exact in bf16 and fp32 when the library wrote the scales).
+ * Rows t >= len[b] are left untouched. */
 TB_API tb_status tb_read_kv(tb_ctx* ctx, int layer, int start, int count, void* k_out, void* v_out, void* stream);
 
 /* Set / read the per-sequence lengths of a layer (host arrays of `batch`

@@ -3,8 +3,9 @@ values, rows written behind cached ones, and attention over the values.
 
 A block is 16 tokens of one head.  With F the format's largest value (e4m3:
 448, int8: 127) and amax the block's largest finite magnitude, the scale is
-2^e with e = max(-100, smallest integer with amax <= F 2^e); a value is its
-quotient by the scale rounded to the format's nearest (ties to even), times
+2^e with e the smallest integer with amax <= F 2^e, at least -100 and at most 119
+(int8: 121, so that F 2^e is finite in fp32); a value is its quotient by the scale
+rounded to the format's nearest (ties to even; magnitudes above F to F), times
 the scale.  A block that holds rows already keeps the larger of its old and
 the new exponent, and its rows are rounded again at it.
 """
@@ -16,6 +17,7 @@ import numpy as np
 
 BLOCK = 16
 E_MIN = -100
+E_MAX = {"e4m3": 119, "int8": 121}
 LARGEST = {"e4m3": 448.0, "int8": 127.0}
 
 
@@ -26,7 +28,7 @@ def exponent(rows: np.ndarray, fmt: str) -> int:
     if amax == 0.0:
         return E_MIN
     e = E_MIN
-    while LARGEST[fmt] * 2.0 ** e < amax:
+    while e < E_MAX[fmt] and LARGEST[fmt] * 2.0 ** e < amax:
         e += 1
     return e
 

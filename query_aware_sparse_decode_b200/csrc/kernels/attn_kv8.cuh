@@ -22,39 +22,43 @@ struct AttnKv8Params : AttnParams {
 // sequence has: the shortest chunks (whole mask words) that keep the call's CTAs
 // within one wave of kKv8CtasPerSm per SM, or, where these would be longer than
 // kKv8LongChunk, within as many waves as bring them down to it (dense B = 4, L =
-// 131072: 203 us in one wave of 7296 tokens, 183 us with 2048; short chunks in
-// several waves lose: B = 16, L = 8192, 66 us either way).
+// 131072: 203 us in one wave of 7296 tokens, 183 us with 2048; shorter chunks
+// lose again: 173 us with 512 when 2048 takes 163).  A batch with more (sequence,
+// KV head) pairs than one wave has CTAs takes chunks of kKv8LongChunk.
 constexpr int kKv8CtasPerSm = 4;
 constexpr int kKv8MinChunk = 128;    // a tile or two a warp; the FMA kernel of fp32 queries takes
 constexpr int kKv8MinChunkF32 = 32;  // its tokens one by one: B = 2, L = 512: 16.4 us with 128, 9.6 us with 32
 constexpr int kKv8LongChunk = 2048;
 inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch, int max_splits, int min_chunk,
                            int* chunk_out, int* nsplit_out) {
-  long long total = 0;
-  int longest = 1;
+  long long total = 0, longest = 1, used = 0;
   for (int b = 0; b < batch; ++b) {
     total += lens[b];
     longest = lens[b] > longest ? lens[b] : longest;
+    used += lens[b] > 0;
   }
   const long long wave = (long long)kKv8CtasPerSm * num_sms;
   const long long one = (total * kv_heads + wave - 1) / wave;  // the chunk of one wave
-  const long long slots = wave * ((one + kKv8LongChunk - 1) / kKv8LongChunk > 0 ? (one + kKv8LongChunk - 1) / kKv8LongChunk : 1);
-  long long chunk = (total * kv_heads + slots - 1) / slots;
+  const long long waves = one > kKv8LongChunk ? (one + kKv8LongChunk - 1) / kKv8LongChunk : 1;
+  const long long slots = wave * waves;
+  const bool fits = used * kv_heads <= slots;
+  long long chunk = fits ? (total * kv_heads + slots - 1) / slots : kKv8LongChunk;
   const long long least = (longest + max_splits - 1) / max_splits;
   chunk = chunk < least ? least : chunk;
-  chunk = chunk < min_chunk ? min_chunk : (chunk + 31) / 32 * 32;
-  for (;;) {
-    long long n = 0, next = longest + 31;  // the CTAs, and the next chunk that has fewer
+  chunk = chunk < min_chunk ? min_chunk : chunk;
+  chunk = (chunk + 31) / 32 * 32;
+  while (fits && chunk < longest) {
+    long long n = 0, next = longest;  // the CTAs, and the next chunk that has fewer
     for (int b = 0; b < batch; ++b) {
       const long long ns = (lens[b] + chunk - 1) / chunk;
       n += ns;
       if (ns > 1) {
-        const long long c = ((lens[b] + ns - 2) / (ns - 1) + 31) / 32 * 32;
+        const long long c = (lens[b] + ns - 2) / (ns - 1);
         next = c < next ? c : next;
       }
     }
-    if (n * kv_heads <= slots || chunk >= longest) break;
-    chunk = next > chunk ? next : chunk + 32;
+    if (n * kv_heads <= slots) break;
+    chunk = (next + 31) / 32 * 32;  // > chunk: at least one sequence has a split less
   }
   *chunk_out = (int)chunk;
   *nsplit_out = (int)((longest + chunk - 1) / chunk);

@@ -5,7 +5,7 @@
 // 16 tokens of an aligned block share one fp32 scale.  With F the largest code
 // value (e4m3: 448, int8: 127) and amax the block's largest finite magnitude
 //
-//   e = max(-100, smallest integer with amax <= F 2^e),  scale = 2^e,
+//   e = smallest integer with amax <= F 2^e, in [-100, 119] (int8: 121),  scale = 2^e,
 //   code = x 2^-e rounded to the format's nearest value, ties to even.
 //
 // A power of two makes the scaling exact: a code differs from x only by its own
@@ -14,7 +14,8 @@
 // block whose scale grows when a token joins it re-rounds its older codes by a
 // power of two (e4m3 codes then change only where they become subnormal; int8
 // codes lose at most half a step of each scale passed, under one final step in
-// all).  It costs up to one bit of the int8 range.  Blocks of 16 tokens never
+// all).  It costs up to one bit of the int8 range.  The upper limit keeps F 2^e
+// finite: the few values above it (2.98e38, int8 3.38e38) are stored as it.  Blocks of 16 tokens never
 // cross a page (pages hold a power of two >= 16 tokens), so the scale of cache
 // row r is scale[r / 16] in dense and paged caches.
 #pragma once
@@ -25,6 +26,8 @@ namespace tb {
 
 constexpr int kKv8Block = TB_KV8_BLOCK;
 constexpr int kKv8MinExp = -100;
+template <int FMT>
+constexpr int kKv8MaxExp = FMT == TB_KV8_E4M3 ? 119 : 121;
 constexpr int kFmtE4m3 = TB_KV8_E4M3;
 constexpr int kFmtInt8 = TB_KV8_INT8;
 
@@ -37,7 +40,7 @@ __device__ __forceinline__ int kv8_exponent(float amax) {
   const int ex = (int)(u >> 23) - 127;
   const uint32_t mant = u & 0x7FFFFFu;
   const int e = FMT == kFmtE4m3 ? ex - 8 + (mant > 0x600000u) : ex - 6 + (mant > 0x7E0000u);
-  return e < kKv8MinExp ? kKv8MinExp : e;
+  return e < kKv8MinExp ? kKv8MinExp : e > kKv8MaxExp<FMT> ? kKv8MaxExp<FMT> : e;
 }
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float kv8_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -50,7 +53,7 @@ __device__ __forceinline__ float kv8_mag(float x) {
 __device__ __forceinline__ bool kv8_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // code of x * inv (inv = 1 / scale, a power of two): rounded to nearest even,
-// infinities to the largest code value, NaN to zero
+// infinities and values above the largest code to it, NaN to zero
 template <int FMT>
 __device__ __forceinline__ uint8_t kv8_encode(float y) {
   if (y != y) y = 0.f;
@@ -287,6 +290,7 @@ __device__ __forceinline__ void kv8_store_rows(const Kv8WriteBf16Params& p, int 
     }
   uint32_t top = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
   const bool odd = top >= 0x7F80u;  // an infinity or a NaN
+  const bool clamp = top > (FMT == kFmtE4m3 ? 0x7F60u : 0x7F7Eu);  // these, or a value above F 2^e
   if (odd) {
     float a = 0.f;
 #pragma unroll
@@ -316,7 +320,7 @@ __device__ __forceinline__ void kv8_store_rows(const Kv8WriteBf16Params& p, int 
       for (int i = 0; i < NP; ++i) {
         const uint4 w = x[h][i];
         uint2 c;
-        if (!odd) {
+        if (!clamp) {
           c.x = kv8_encode4<FMT>(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), inv);
           c.y = kv8_encode4<FMT>(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w), inv);
         } else {

@@ -728,6 +728,7 @@ TB_API tb_status tb_bind_layer_kv8_paged(tb_ctx* ctx, int layer, int format, voi
   if (page_size < 16 || (page_size & (page_size - 1)) != 0 || num_pages < 1 || max_pages < 1) return TB_ERR_SHAPE;
   if ((long long)max_pages * page_size < c.max_len) return TB_ERR_SHAPE;
   if ((long long)num_pages * c.n_kv_heads * page_size >= (1LL << 31)) return TB_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(page_table) & 3u) return TB_ERR_SHAPE;
   int shift = 0;
   while ((1 << shift) < page_size) ++shift;
   return bind_kv8(ctx, layer, format, k_pool, v_pool, k_scale, v_scale,
@@ -989,6 +990,7 @@ TB_API tb_status tb_append_kv(tb_ctx* ctx, int layer, const void* k_new, const v
   LayerState& ls = ctx->layers[layer];
   if (ls.kv8) {  // one row a sequence, [B][Hkv][D]
     if (!k_new || !v_new) return TB_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new)) return TB_ERR_SHAPE;  // rows are read 16 bytes at a time
     const int64_t strides[3] = {(int64_t)c.n_kv_heads * c.head_dim, c.head_dim, c.head_dim};
     int32_t one[TB_MAX_BATCH];
     std::fill(one, one + c.batch, 1);

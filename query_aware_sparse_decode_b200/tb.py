@@ -315,13 +315,14 @@ class Context:
         if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the context on cuda:{self._index}")
 
-    def _on_device(self, call, what: str, stream) -> None:
-        """call(stream handle) with the context's device current."""
+    def _on_device(self, what: str, stream, *args) -> None:
+        """lib().<what>(context, *args, stream handle) with the context's device current."""
+        call = getattr(lib(), what)
         if torch._C._cuda_getDevice() == self._index:
-            _check(call(_stream(stream)), what)
+            _check(call(self._h, *args, _stream(stream)), what)
         else:
             with torch.cuda.device(self._index):
-                _check(call(_stream(stream)), what)
+                _check(call(self._h, *args, _stream(stream)), what)
 
     def _check_kv8(self, lead, rows, k, v, k_scale, v_scale, kimp_cache, w_k) -> int:
         c = self.cfg
@@ -374,10 +375,8 @@ class Context:
             raise ValueError(f"counts must be {B} numbers in [0, {n}], got {counts}")
         if n == 0:
             return
-        ks, vs = _row_strides("k", k), _row_strides("v", v)
-        arr = self._lens_type(*counts)
-        self._on_device(lambda st: lib().tb_append_kv_rows(self._h, layer, k.data_ptr(), v.data_ptr(), ks, vs, arr, st),
-                        "tb_append_kv_rows", stream)
+        self._on_device("tb_append_kv_rows", stream, layer, k.data_ptr(), v.data_ptr(), _row_strides("k", k),
+                        _row_strides("v", v), self._lens_type(*counts))
 
     def read_kv(self, layer: int, start: int, count: int, k_out=None, v_out=None, stream=None) -> None:
         """Rows [start, start + count) of an 8-bit layer as values into k_out
@@ -390,8 +389,7 @@ class Context:
             self._expect("v_out", v_out, (B, H, count, D), self._kv_dtype)
         if count == 0 and not (k_out is None and v_out is None):
             return
-        ko, vo = _ptr(k_out), _ptr(v_out)
-        self._on_device(lambda st: lib().tb_read_kv(self._h, layer, start, count, ko, vo, st), "tb_read_kv", stream)
+        self._on_device("tb_read_kv", stream, layer, start, count, _ptr(k_out), _ptr(v_out))
 
     def selection_cache(self, layer: int):
         """Allocate (zero-filled) and bind layer `layer`'s selection cache;

@@ -212,6 +212,23 @@ def test_edge_values(fmt):
         assert np.array_equal(codes[0, 0, :160] * np.repeat(s[0, 0, :10], 16)[:, None], c.val[name][0, 0, :160])
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_the_top_of_the_range_stays_finite(fmt):
+    """bf16 rows with the type's largest values, beside ordinary blocks."""
+    c = Case(fmt, Hq=1, Hkv=1, B=1, max_len=256)
+    top = float(torch.finfo(torch.bfloat16).max)
+    k = c.rng.normal(size=(1, 1, 40, c.D))
+    k[0, 0, 3, ::7], k[0, 0, 17, 5], k[0, 0, 18, 6] = top, -top, 2.9e38
+    c.append([40], k=k, v=-k)
+    out = torch.zeros((1, 1, 40, c.D), dtype=torch.bfloat16, device="cuda")
+    c.ctx.read_kv(0, 0, 40, out)
+    torch.cuda.synchronize()
+    assert c.ctx.check_status() == 0
+    assert np.array_equal(host(out)[0, 0], c.val["k"][0, 0, :40]) and bool(torch.isfinite(out).all())
+    codes, s = c.cached()[1]
+    assert np.array_equal(codes[0, 0, :40] * np.repeat(s[0, 0, :3], 16)[:40, None], c.val["v"][0, 0, :40])
+
+
 def test_not_a_number_and_infinity_are_stored_finite_and_flagged():
     c = Case("e4m3", Hq=1, Hkv=1, B=1, max_len=256)
     k = c.rng.normal(size=(1, 1, 20, c.D))
@@ -564,6 +581,75 @@ def test_sharded_step_over_8_bit_caches():
         whole.check_attention(q, sets, o, None)
 
 
+def test_reused_selections_and_prefill_rows_on_8_bit_layers():
+    """Amortised selection and the row selection of a prefill read K_imp only: an
+    8-bit layer and a bf16 one with the same K_imp choose the same tokens."""
+    c = Case("int8", B=2, max_len=512, layers=2, seed=12)
+    c.append((400, 130))
+    kb, vb = (torch.randn((2, 2, 512, 128), device="cuda").bfloat16() for _ in range(2))
+    torch.cuda.synchronize()
+    kimp = c.kimp.clone()
+    c.ctx.bind_layer(1, kb, vb, kimp, c.w)
+    c.ctx.set_seq_lens(1, c.lens)
+    rows = dev(c.rng.normal(size=(c.B * c.Hq, 1, 20, c.dimp)), "bf16")
+    masks = [torch.zeros((c.B, c.Hq, 20, 16), dtype=torch.int32, device="cuda") for _ in range(2)]
+    for layer in (0, 1):
+        c.ctx.select_prefill(layer, rows, 100, 20, masks[layer])
+    torch.cuda.synchronize()
+    assert torch.equal(masks[0], masks[1]) and int(masks[0].ne(0).sum()) > 0
+    caches = [c.ctx.selection_cache(layer) for layer in (0, 1)]
+    c.ctx.set_reuse(0.5, 3, 1)
+    qi = dev(c.rng.normal(size=(c.B * c.Hq, 1, 1, c.dimp)), "bf16")
+    q = dev(c.rng.normal(size=(c.B, c.Hq, c.D)), "bf16")
+    for step in range(3):
+        k, v = c.step_rows()
+        got = []
+        for layer in (0, 1):
+            out = torch.empty_like(q)
+            c.ctx.decode_step(layer, k, v, q, qi, out)
+            got.append(sets_from_mask(c.ctx.step_masks(c.Hq), c.ctx.seq_lens(layer)))
+        c.track(host(k)[:, :, None], host(v)[:, :, None], [1, 1])
+        torch.cuda.synchronize()
+        # the appended rows' K_imp differ by fp32 rounding (another order of the same sum)
+        assert all(len(np.setxor1d(got[0][x], got[1][x])) <= 2 for x in got[0])
+    assert c.ctx.check_status() == 0 and len(caches) == 2
+
+
+def test_offsets_past_32_bits():
+    """A cache whose codes pass 2^32 bytes: rows written, read and attended near its end."""
+    n = 4194304 + 512
+    c = Case("e4m3", B=1, Hq=8, Hkv=8, max_len=n, dense=True, seed=2)
+    L0 = n - 300
+    c.val = {x: np.zeros((1, 8, 512, 128)) for x in "kv"}   # the oracle's window: the last rows
+    c.ctx.set_seq_lens(0, [L0])
+    k, v = (dev(c.rng.normal(size=(1, 8, 200, 128)), "bf16") for _ in range(2))
+    c.ctx.append_kv_rows(0, k, v)
+    kn, vn = c.step_rows()
+    q = dev(c.rng.normal(size=(1, 8, 128)), "bf16")
+    c.ctx.append_kv(0, kn, vn)
+    assert c.ctx.seq_lens(0) == [L0 + 201]
+    base = L0 // 16 * 16
+    assert base == L0 - 4   # the rows start inside a block whose older rows are zero
+    for g in range(8):
+        for x, a, b in (("k", k, kn), ("v", v, vn)):
+            w, e = O8.append(np.zeros((512, 128)), np.full(32, O8.E_MIN), 4, host(a)[0, g], "e4m3")
+            c.val[x][0, g], _ = O8.append(w, e, 204, host(b)[0, g][None], "e4m3")
+    ko = torch.zeros((1, 8, 201, 128), dtype=torch.bfloat16, device="cuda")
+    c.ctx.read_kv(0, L0, 201, ko)
+    mask = torch.zeros((1, 8, n // 32), dtype=torch.int32, device="cuda")
+    bits = np.zeros((8, 512), bool)
+    for h in range(8):
+        bits[h, 4:205] = c.rng.random(201) < 0.3
+        for t in np.nonzero(bits[h])[0] + base:
+            mask[0, h, t // 32] |= int(np.uint32(1 << (int(t) % 32)).astype(np.int32))
+    out, lse = torch.empty_like(q), torch.empty((1, 8), device="cuda")
+    c.ctx.sparse_attn(0, q, mask, TB.TB_MASK_PER_HEAD, out, lse)
+    torch.cuda.synchronize()
+    assert c.ctx.check_status() == 0
+    assert np.array_equal(host(ko)[0], c.val["k"][0, :, 4:205])
+    c.check_attention(q, {(0, h): np.nonzero(bits[h])[0] for h in range(8)}, out, lse)
+
+
 # ------------------------------------------------------------------ use
 def test_layers_of_both_kinds_in_one_context_and_rebinding():
     c = Case("e4m3", B=2, layers=2, dense=True, max_len=512)
@@ -674,6 +760,10 @@ def test_refusals():
     with pytest.raises(TB.TBError) as e:           # rows not 16-byte aligned
         c.ctx.append_kv_rows(0, odd[4:4 + 2 * 2 * 300 * 128].view(2, 2, 300, 128), k, [10, 10])
     assert e.value.status == 2
+    with pytest.raises(TB.TBError) as e:
+        c.ctx.append_kv(0, odd[4:4 + 512].view(2, 2, 128), k[:, :, 0].contiguous())
+    assert e.value.status == 2 and c.ctx.seq_lens(0) == [300, 0]
+    assert L.tb_bind_layer_kv8_paged(h, 1, 1, *ptr[:4], 8, ctypes.c_void_p(c.kimp.data_ptr() + 2), 64, 8, *ptr[4:]) == 2
     out = torch.zeros((2, 2, 10, 128), dtype=torch.bfloat16, device="cuda")
     for start, n, want in ((-1, 10, 1), (508, 10, 3)):
         with pytest.raises(TB.TBError) as e:

@@ -28,9 +28,14 @@ def test_rounding_equals_the_library_cast(fmt):
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_exponent_is_the_smallest_that_fits(fmt):
     big = O8.LARGEST[fmt]
-    for top in (1e-3, 1.0, big, np.nextafter(big, 1e9), big * 2, 3.3e38, 447.0, 126.5):
+    for top in (1e-3, 1.0, big, np.nextafter(big, 1e9), big * 2, 2.9e38, 447.0, 126.5):
         e = O8.exponent(np.array([top, -top / 3]), fmt)
         assert top <= big * 2.0 ** e and (top > big * 2.0 ** (e - 1))
+    # the largest finite values saturate at F 2^e, which fp32 and bf16 hold
+    top = float(np.finfo(np.float32).max)
+    assert O8.exponent(np.array([top]), fmt) == O8.E_MAX[fmt] and np.isfinite(np.float32(big * 2.0 ** O8.E_MAX[fmt]))
+    val, _ = O8.quantise(np.full((16, 4), top), fmt)
+    assert np.all(val == big * 2.0 ** O8.E_MAX[fmt])
     assert O8.exponent(np.zeros(4), fmt) == O8.E_MIN
     assert O8.exponent(np.array([1e-38, 0]), fmt) == O8.E_MIN
     assert O8.exponent(np.array([np.inf, np.nan, 1.0]), fmt) == O8.exponent(np.array([1.0]), fmt)
