@@ -304,6 +304,16 @@ __device__ __forceinline__ void cp_async_4(uint32_t smem, const void* gmem) {
 __device__ __forceinline__ void cp_async_16u(uint32_t smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem), "l"(gmem) : "memory");
 }
+// the same for data that is read once: its lines are the first to leave L2
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp_async_16_once(uint32_t smem, const void* gmem, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "l"(policy)
+               : "memory");
+}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -726,6 +736,7 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
   const uint8_t* Kb = reinterpret_cast<const uint8_t*>(p.k_cache) + 16 * c_part;
   const uint32_t ring = smem_u32(smem) + warp * kVoteKv8Stages * STAGE;
   const uint32_t scales = smem_u32(smem) + kVoteWarps * kVoteKv8Stages * STAGE + warp * kVoteKv8Stages * 16;
+  const uint64_t policy = evict_first_policy();  // the logits stay in L2 for the reduce pass
   const int my_n = (t1 - t0 - warp * kAttnTile + kVoteWarps * kAttnTile - 1) / (kVoteWarps * kAttnTile);  // may be <= 0
   auto issue = [&](int it) {
     const int tt = t0 + (warp + it * kVoteWarps) * kAttnTile;
@@ -744,8 +755,8 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
 #pragma unroll
     for (int r = 0; r < kAttnTile / CR; ++r) {
       const int rr = c_row + CR * r;
-      cp_async_16u(ring + stage * STAGE + rr * D + ((c_part ^ kv8_swizzle_k<D>(rr)) << 4),
-                   Kb + (size_t)(row + min(rr, last)) * D);
+      cp_async_16_once(ring + stage * STAGE + rr * D + ((c_part ^ kv8_swizzle_k<D>(rr)) << 4),
+                       Kb + (size_t)(row + min(rr, last)) * D, policy);
     }
   };
 #pragma unroll
