@@ -476,10 +476,10 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const Kv8ReadParams p) {
       kv8_decode4<FMT>(c[kv][u][0], x);
       if constexpr (CW == 2) {
         kv8_decode4<FMT>(c[kv][u][CW - 1], y);
-        *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f),
-                                                    pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f));
+        __stcs(reinterpret_cast<uint4*>(out), make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f),
+                                                         pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f)));
       } else {
-        *reinterpret_cast<float4*>(out) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+        __stcs(reinterpret_cast<float4*>(out), make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f));
       }
     }
   }
