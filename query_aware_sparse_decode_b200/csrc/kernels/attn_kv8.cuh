@@ -291,7 +291,8 @@ constexpr int attn_kv8_smem() {
 }
 // 16-byte pieces of a cached row are stored at piece ^ swizzle(row), so that the
 // lanes of a shared-memory phase touch different banks: for K two rows' pieces
-// tq, for V rows 0, 2, 4, 6 (+ 1) of two neighbouring pieces.
+// tq, for V rows 0, 2, 4, 6 (+ 1) of two neighbouring pieces.  Both are linear over
+// xor in rows without common bits, so that a lane's share is a constant.
 // log2 of a V scale; finite or -inf, so that a masked token's weight stays zero over any scale
 __device__ __forceinline__ float kv8_log2_scale(float vs) { return fminf(__log2f(vs), 1e30f); }
 template <int D>
@@ -382,11 +383,17 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   const uint8_t* Vb = reinterpret_cast<const uint8_t*>(p.v_cache) + 16 * c_part;
   uint8_t* mine = smem + warp * attn_kv8_warp_bytes<D, DENSE>();
   const uint32_t ring = smem_u32(mine);
-  const uint32_t c_dst = ring + c_row * D, k_src = ring + grp * D, v_src = ring + VOFF + 2 * tq * D + grp * VB % 16;
+  // (a tile's rows differ from the lane's first by multiples of CR, 8 or 1, which
+  // share no bits with it)
+  const uint32_t ck_dst = ring + c_row * D + ((c_part ^ kv8_swizzle_k<D>(c_row)) << 4);
+  const uint32_t cv_dst = ring + VOFF + c_row * D + ((c_part ^ kv8_swizzle_v<D>(c_row)) << 4);
+  const uint32_t k_src = ring + grp * D + ((tq ^ kv8_swizzle_k<D>(grp)) << 4);
+  const uint32_t v_src = ring + VOFF + 2 * tq * D + (((grp * VB >> 4) ^ kv8_swizzle_v<D>(2 * tq)) << 4) + grp * VB % 16;
   // per stage: DENSE: the block's (ks, vs); else the 16 tokens' (ks log2e/sqrt(D), log2 vs, head bits)
   const uint32_t meta = ring + kKv8Stages * STAGE;
 
-  const uint32_t head_bits = ((1u << GS) - 1u) >> (2 * tq) & 3u;
+  const uint32_t group_bits = (1u << GS) - 1u;
+  const uint32_t head_bit[2] = {(1u << 2 * tq) & group_bits, (2u << 2 * tq) & group_bits};
   float o[MT][4];  // dims grp D/8 + 2mt (+1), heads 2tq + {0,1}
 #pragma unroll
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -399,13 +406,12 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
 #pragma unroll
     for (int r = 0; r < kAttnTile / CR; ++r) {
       const size_t src = (size_t)rows[r] * D;
-      const uint32_t dst = c_dst + off + r * CR * D;
-      cp_async_16u(dst + ((c_part ^ kv8_swizzle_k<D>(c_row + CR * r)) << 4), Kb + src);
-      cp_async_16u(dst + VOFF + ((c_part ^ kv8_swizzle_v<D>(c_row + CR * r)) << 4), Vb + src);
+      cp_async_16u((ck_dst ^ kv8_swizzle_k<D>(CR * r) << 4) + (off + r * CR * D), Kb + src);
+      cp_async_16u((cv_dst ^ kv8_swizzle_v<D>(CR * r) << 4) + (off + r * CR * D), Vb + src);
     }
   };
 
-  // ---- the warp's tiles: issue(it) starts the copies of tile `it`, false when there is none
+  // ---- the warp's tiles: issue(it, stage) starts the copies of tile `it`, false when there is none
   const int dense_tiles = (t1 - t0 + kAttnTile - 1) / kAttnTile;
   // list state: the segment being cut (list entries [pos, cnt)), the waiting tokens
   // (lanes 0 .. wait_n - 1), the next segment [seg, seg_end) and what is requested of it
@@ -495,8 +501,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     ev = __uint_as_float(blk.z);
     hb = v >> 8;
   };
-  auto issue = [&](int it) -> bool {
-    const uint32_t stage = (uint32_t)(it % kKv8Stages);
+  auto issue = [&](int it, uint32_t stage) -> bool {
     uint32_t rows[kAttnTile / CR];
     if constexpr (DENSE) {
       const int tile = warp + it * kAttnWarps;
@@ -517,23 +522,32 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
       for (int r = 0; r < kAttnTile / CR; ++r) rows[r] = row + min(c_row + CR * r, last);
     } else {
       const int l16 = lane & 15;
-      while (wait_n + cnt - pos < kAttnTile && seg < seg_end) {
-        if (l16 >= wait_n && l16 < wait_n + cnt - pos) entry(pos + l16 - wait_n, w_row, w_ks, w_ev, w_hb);
-        wait_n += cnt - pos;
-        build();
-      }
-      const int n = min(wait_n + cnt - pos, kAttnTile);
-      if (n == 0) return false;
-      uint32_t row = w_row, hb = w_hb;
-      float ks = w_ks, ev = w_ev;
-      if (l16 >= wait_n && l16 < n) entry(pos + l16 - wait_n, row, ks, ev, hb);
-      pos += n - wait_n;
-      wait_n = 0;
-      const uint32_t first = __shfl_sync(0xffffffffu, row, 0);
-      if (l16 >= n) {  // past the last token: its row again, for no head
-        row = first;
-        ks = ev = 0.f;
-        hb = 0u;
+      uint32_t row, hb;
+      float ks, ev;
+      if (wait_n == 0 && cnt - pos >= kAttnTile) {  // most tiles: 16 entries of the list
+        entry(pos + l16, row, ks, ev, hb);
+        pos += kAttnTile;
+      } else {
+        while (wait_n + cnt - pos < kAttnTile && seg < seg_end) {
+          if (l16 >= wait_n && l16 < wait_n + cnt - pos) entry(pos + l16 - wait_n, w_row, w_ks, w_ev, w_hb);
+          wait_n += cnt - pos;
+          build();
+        }
+        const int n = min(wait_n + cnt - pos, kAttnTile);
+        if (n == 0) return false;
+        row = w_row;
+        hb = w_hb;
+        ks = w_ks;
+        ev = w_ev;
+        if (l16 >= wait_n && l16 < n) entry(pos + l16 - wait_n, row, ks, ev, hb);
+        pos += n - wait_n;
+        wait_n = 0;
+        const uint32_t first = __shfl_sync(0xffffffffu, row, 0);
+        if (l16 >= n) {  // past the last token: its row again, for no head
+          row = first;
+          ks = ev = 0.f;
+          hb = 0u;
+        }
       }
       if (lane < 16)
         *reinterpret_cast<uint4*>(mine + kKv8Stages * STAGE + (stage * kAttnTile + lane) * 16) =
@@ -549,26 +563,27 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   int queued = 0;  // tiles whose copies have started
 #pragma unroll
   for (int s = 0; s < kKv8Stages - 1; ++s) {
-    if (issue(s)) ++queued;
+    if (issue(s, s)) ++queued;
     cp_async_commit();
   }
   uint32_t qb[D / 16][2];
   float qs[2];
   load_q_f16<D, GS>(p.q, (size_t)b * p.Hq + g * GS, grp, tq, qb, qs);
-  for (int it = 0; it < queued; ++it) {
+  uint32_t stage = 0;
+  for (int it = 0; it < queued; ++it, stage = stage == kKv8Stages - 1 ? 0 : stage + 1) {
     __syncwarp();  // the stage refilled now has been read by every lane
-    if (queued == it + kKv8Stages - 1 && issue(queued)) ++queued;
+    if (queued == it + kKv8Stages - 1 && issue(queued, stage == 0 ? kKv8Stages - 1 : stage - 1)) ++queued;
     cp_async_commit();
     cp_async_wait<kKv8Stages - 1>();
     __syncwarp();  // the pieces come from other lanes
-    const uint32_t stage = (uint32_t)(it % kKv8Stages), off = stage * STAGE;
+    const uint32_t off = stage * STAGE;
     // ---- S^T = K Q^T: s[0..1] = token grp, s[2..3] = grp + 8; heads 2tq + {0,1}
     float s[4];
     {
       uint4 ka[KLD], kb[KLD];  // rows grp, grp + 8
 #pragma unroll
       for (int i = 0; i < KLD; ++i) {
-        const uint32_t at = k_src + off + (((tq + 4 * i) ^ kv8_swizzle_k<D>(grp)) << 4);
+        const uint32_t at = (k_src ^ i << 6) + off;
         ka[i] = lds16(at);
         kb[i] = lds16(at + 8 * D);
       }
@@ -576,7 +591,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     }
     // x = s f; d = x - T; z = d + log2 vs + T - R + 15
     float f[2][2], ev[2];
-    uint32_t hb[2];  // tokens grp and grp + 8: bits of the lane's two heads
+    uint32_t hb[2];  // tokens grp and grp + 8: their heads
     bool masked = true;
     if constexpr (DENSE) {
       const uint2 sc = lds8(meta + stage * (kAttnTile * 16));
@@ -586,8 +601,8 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
       for (int e = 0; e < 2; ++e) f[0][e] = f[1][e] = qs[e] * (ks * p.scale_log2);
       const int left = ks == ks ? t1 - t0 - (warp + it * kAttnWarps) * kAttnTile : 0;
       masked = left < kAttnTile;
-      hb[0] = grp < left ? 3u : 0u;
-      hb[1] = grp + 8 < left ? 3u : 0u;
+      hb[0] = grp < left ? ~0u : 0u;
+      hb[1] = grp + 8 < left ? ~0u : 0u;
     } else {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -595,7 +610,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
         ev[r] = __uint_as_float(e.y);
         f[r][0] = qs[0] * __uint_as_float(e.x);
         f[r][1] = qs[1] * __uint_as_float(e.x);
-        hb[r] = e.z >> (2 * tq) & head_bits;
+        hb[r] = e.z;
       }
     }
     float d[4], z[4];
@@ -606,7 +621,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
         for (int e = 0; e < 2; ++e) {
           const int j = 2 * r + e;
           d[j] = fmaf(s[j], f[r][e], -ref[e]);
-          if (masked && !(hb[r] >> e & 1u)) d[j] = kNegInf;
+          if (masked && !(hb[r] & head_bit[e])) d[j] = kNegInf;
           z[j] = d[j] + (ev[r] + lift[e]);
         }
     };
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
         float mt = kNegInf, rt = kNegInf;  // the tile's largest x and x + log2 vs of the head
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          if (!masked || (hb[r] >> e & 1u)) {
+          if (!masked || (hb[r] & head_bit[e])) {
             mt = fmaxf(mt, s[2 * r + e] * f[r][e]);
             rt = fmaxf(rt, s[2 * r + e] * f[r][e] + ev[r]);
           }
@@ -650,8 +665,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     uint32_t vc[4][VW];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = (r & 1) + 8 * (r >> 1);  // + 2tq
-      const uint32_t at = v_src + off + row * D + (((grp * VB >> 4) ^ kv8_swizzle_v<D>(2 * tq + row)) << 4);
+      const uint32_t at = v_src + off + ((r & 1) + 8 * (r >> 1)) * D;  // row 2tq + {0, 1, 8, 9}
       if constexpr (VW == 4) {
         const uint4 v = lds16(at);
         vc[r][0] = v.x;
