@@ -273,7 +273,7 @@ __device__ __forceinline__ void kv8_scores(const uint4 (&ka)[D / 64], const uint
 }
 
 // Ring of one warp: kKv8Stages tiles of 16 K and V rows.
-constexpr int kKv8Stages = 3;
+constexpr int kKv8Stages = 2;
 constexpr int kKv8Seg = 256;  // tokens of a warp's gather list
 template <int D>
 constexpr int kv8_stage_bytes() { return 2 * kAttnTile * D; }
