@@ -21,15 +21,26 @@ struct AttnKv8Params : AttnParams {
 // Split of the 8-bit attention (host side), counting the tokens that each
 // sequence has: the shortest chunks (whole mask words) that keep the call's CTAs
 // within one wave of kKv8CtasPerSm per SM, or, where these would be longer than
-// kKv8LongChunk, within as many waves as bring them down to it (dense B = 4, L =
-// 131072: 203 us in one wave of 7296 tokens, 183 us with 2048; shorter chunks
-// lose again: 173 us with 512 when 2048 takes 163).  A batch with more (sequence,
-// KV head) pairs than one wave has CTAs takes chunks of kKv8LongChunk.
+// `long_chunk`, within as many waves as bring them down to it.  A batch with more
+// (sequence, KV head) pairs than one wave has CTAs takes chunks of long_chunk.
+//  - Every token: 2048 (B = 4, L = 131072: 163 us, 203 us in one wave of 7296, 173 us with 512).
+//  - Lists: 8192, since a CTA's first tile waits for a chain of mask, row and scale
+//    loads and a sparse chunk has few tiles (the same lengths, one set per KV group with
+//    10 % / 30 % of the tokens: 32.6 / 61.5 us, with 2048 39.9 / 71.0 us; 30 % per head 132
+//    against 141 us).  From 4096 on, chunks are multiples of the four warps' segments.
 constexpr int kKv8CtasPerSm = 4;
-constexpr int kKv8MinChunk = 128;    // a tile or two a warp; the FMA kernel of fp32 queries takes
-constexpr int kKv8MinChunkF32 = 32;  // its tokens one by one: B = 2, L = 512: 16.4 us with 128, 9.6 us with 32
-constexpr int kKv8LongChunk = 2048;
-inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch, int max_splits, int min_chunk,
+constexpr int kKv8Seg = 256;  // tokens of a warp's gather list
+struct Kv8Split {
+  int min_chunk, long_chunk;
+};
+constexpr Kv8Split kKv8SplitDense{128, 2048};  // 128: a tile or two a warp
+constexpr Kv8Split kKv8SplitList{128, 8192};
+constexpr Kv8Split kKv8SplitF32{32, 2048};     // tokens one by one (B = 2, L = 512: 16.4 us with 128, 9.6 us with 32)
+inline long long kv8_round_chunk(long long chunk, const Kv8Split& how) {
+  const long long unit = how.long_chunk > 4096 && chunk >= 4096 ? kAttnWarps * kKv8Seg : 32;
+  return (chunk + unit - 1) / unit * unit;
+}
+inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch, int max_splits, const Kv8Split& how,
                            int* chunk_out, int* nsplit_out) {
   long long total = 0, longest = 1, used = 0;
   for (int b = 0; b < batch; ++b) {
@@ -39,14 +50,13 @@ inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch
   }
   const long long wave = (long long)kKv8CtasPerSm * num_sms;
   const long long one = (total * kv_heads + wave - 1) / wave;  // the chunk of one wave
-  const long long waves = one > kKv8LongChunk ? (one + kKv8LongChunk - 1) / kKv8LongChunk : 1;
+  const long long waves = one > how.long_chunk ? (one + how.long_chunk - 1) / how.long_chunk : 1;
   const long long slots = wave * waves;
   const bool fits = used * kv_heads <= slots;
-  long long chunk = fits ? (total * kv_heads + slots - 1) / slots : kKv8LongChunk;
+  long long chunk = fits ? (total * kv_heads + slots - 1) / slots : how.long_chunk;
   const long long least = (longest + max_splits - 1) / max_splits;
   chunk = chunk < least ? least : chunk;
-  chunk = chunk < min_chunk ? min_chunk : chunk;
-  chunk = (chunk + 31) / 32 * 32;
+  chunk = kv8_round_chunk(chunk < how.min_chunk ? how.min_chunk : chunk, how);
   while (fits && chunk < longest) {
     long long n = 0, next = longest;  // the CTAs, and the next chunk that has fewer
     for (int b = 0; b < batch; ++b) {
@@ -58,7 +68,7 @@ inline void attn_split_kv8(int num_sms, int kv_heads, const int* lens, int batch
       }
     }
     if (n * kv_heads <= slots) break;
-    chunk = (next + 31) / 32 * 32;  // > chunk: at least one sequence has a split less
+    chunk = kv8_round_chunk(next, how);  // > chunk: at least one sequence has a split less
   }
   *chunk_out = (int)chunk;
   *nsplit_out = (int)((longest + chunk - 1) / chunk);
@@ -272,9 +282,10 @@ __device__ __forceinline__ void kv8_scores(const uint4 (&ka)[D / 64], const uint
   for (int j = 0; j < 4; ++j) s[j] += s1[j];
 }
 
-// Ring of one warp: kKv8Stages tiles of 16 K and V rows.
+// Ring of one warp, in tiles of 16 K and V rows (three are as fast for lists and slower
+// for dense calls, a step over 16 x 8192 tokens 56.5 us against 54.4; four leave three
+// CTAs an SM and lose everywhere).
 constexpr int kKv8Stages = 2;
-constexpr int kKv8Seg = 256;  // tokens of a warp's gather list
 template <int D>
 constexpr int kv8_stage_bytes() { return 2 * kAttnTile * D; }
 // per warp: the ring, per stage the tokens' (ks, log2 vs, head bits), and for a
@@ -289,12 +300,12 @@ constexpr int attn_kv8_smem() {
   constexpr int merge = kAttnWarps * GS * (D + 2) * 4;
   return work > merge ? work : merge;
 }
+// log2 of a V scale; finite or -inf, so that a masked token's weight stays zero over any scale
+__device__ __forceinline__ float kv8_log2_scale(float vs) { return fminf(__log2f(vs), 1e30f); }
 // 16-byte pieces of a cached row are stored at piece ^ swizzle(row), so that the
 // lanes of a shared-memory phase touch different banks: for K two rows' pieces
 // tq, for V rows 0, 2, 4, 6 (+ 1) of two neighbouring pieces.  Both are linear over
 // xor in rows without common bits, so that a lane's share is a constant.
-// log2 of a V scale; finite or -inf, so that a masked token's weight stays zero over any scale
-__device__ __forceinline__ float kv8_log2_scale(float vs) { return fminf(__log2f(vs), 1e30f); }
 template <int D>
 __device__ __forceinline__ int kv8_swizzle_k(int row) { return D == 128 ? (row & 1) << 2 : 0; }
 template <int D>

@@ -456,7 +456,8 @@ static tb_status launch_attn(tb_ctx* ctx, int layer, const void* q, const uint32
   int chunk = 0;
   if (ls.kv8)
     attn_split_kv8(ctx->num_sms, c.n_kv_heads, ls.lens, c.batch, ctx->lay.max_splits,
-                   c.kv_dtype == TB_BF16 ? kKv8MinChunk : kKv8MinChunkF32, &chunk, &p.nsplit);
+                   c.kv_dtype != TB_BF16 ? kKv8SplitF32 : mode == TB_MASK_DENSE ? kKv8SplitDense : kKv8SplitList, &chunk,
+                   &p.nsplit);
   else if (!attn_split(ctx->num_sms, c.batch * c.n_kv_heads, maxL, &chunk, &p.nsplit))
     return TB_ERR_UNSUPPORTED;
   p.chunk = chunk;
