@@ -211,7 +211,8 @@ TB_API tb_status tb_bind_layer_kv8_paged(tb_ctx* ctx, int layer, int format, voi
  * in elements), V likewise; k, v and every stride must be multiples of 16
  * bytes (TB_ERR_SHAPE).  Rows past counts_host[b] are not read, and cache rows
  * past the new length keep their codes.  TB_ERR_CAPACITY if a sequence
- * would exceed max_len; TB_ERR_UNSUPPORTED for a layer that is not 8-bit. */
+ * would exceed max_len; TB_ERR_UNSUPPORTED for a layer that is not 8-bit;
+ * TB_ERR_INVALID_ARG while another device than the context's is current. */
 TB_API tb_status tb_append_kv_rows(tb_ctx* ctx, int layer, const void* k, const void* v,
                                    const int64_t k_strides[3], const int64_t v_strides[3],
                                    const int32_t* counts_host, void* stream);
@@ -219,7 +220,7 @@ TB_API tb_status tb_append_kv_rows(tb_ctx* ctx, int layer, const void* k, const 
 /* Reads rows [start, start + count) of every (b, KV head) of an 8-bit layer
  * back as code * scale: k_out, v_out [B][Hkv][count][D] kv_dtype (either may
  * be NULL, not both; exact in bf16 and fp32 when the library wrote the scales).
- * Rows t >= len[b] are left untouched. */
+ * Rows t >= len[b] are left untouched.  Errors as for tb_append_kv_rows. */
 TB_API tb_status tb_read_kv(tb_ctx* ctx, int layer, int start, int count, void* k_out, void* v_out, void* stream);
 
 /* Set / read the per-sequence lengths of a layer (host arrays of `batch`

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kv8_f32_kernel(const AttnKv
 #pragma unroll
   for (int hh = 0; hh < GS; ++hh) {
     if (lane == 0) {
-      wm[warp * GS + hh] = m[hh];
+      wm[warp * GS + hh] = l[hh] != l[hh] ? 0.f : m[hh];  // (a NaN logit moves no maximum)
       wl[warp * GS + hh] = l[hh];
     }
 #pragma unroll
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     const int h = 2 * tq + e;
     if (h < GS) {
       if (grp == 0) {
-        wm[warp * GS + h] = ref[e] == kNone ? kNegInf : ref[e];
+        wm[warp * GS + h] = ref[e] == kNone && l_run[e] == 0.f ? kNegInf : ref[e];  // (a NaN logit moves no reference)
         wl[warp * GS + h] = l_run[e];
       }
       const float f = exp2f(-lift[e]);  // back from the weights' reference to T

@@ -397,6 +397,31 @@ def test_attention_with_rising_and_falling_logits():
     c.check_attention(q, c.all_tokens(), out, lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mode", ["head", "dense"])
+def test_a_query_that_is_not_a_number_shows_in_its_head_only(dtype, mode):
+    c = Case("e4m3", dtype, B=2, max_len=512)
+    c.append((300, 40))
+    q = c.rng.normal(size=(c.B, c.Hq, c.D))
+    q[1, 2, 7] = np.nan
+    mask = None
+    if mode == "head":
+        mask = mask_from_sets(random_sets(c, c.Hq, 0.5), c.B, c.Hq, c.max_len)
+    out = torch.zeros((c.B, c.Hq, c.D), dtype=DT[dtype], device="cuda")
+    lse = torch.zeros((c.B, c.Hq), device="cuda")
+    c.ctx.sparse_attn(0, dev(q, dtype), mask, MODES[mode], out, lse)
+    votes = torch.zeros((c.B, c.max_len), device="cuda")
+    if dtype == "bf16":
+        c.ctx.softvote_scores(0, dev(q, dtype), votes)
+    torch.cuda.synchronize()
+    bad = torch.zeros((c.B, c.Hq), dtype=torch.bool, device="cuda")
+    bad[1, 2] = True
+    assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(out).any(-1), bad)
+    assert torch.equal(torch.isnan(lse), bad)
+    if dtype == "bf16":
+        assert bool(torch.isnan(votes[1, :40]).all()) and not bool(torch.isnan(votes[0]).any())
+
+
 @pytest.mark.parametrize("page", [16, 128])
 @pytest.mark.parametrize("mode", ["head", "group", "dense"])
 def test_paged_attention_equals_dense(mode, page):
