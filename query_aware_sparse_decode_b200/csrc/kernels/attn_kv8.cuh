@@ -35,6 +35,9 @@ struct Kv8Split {
 };
 constexpr Kv8Split kKv8SplitDense{128, 2048};  // 128: a tile or two a warp
 constexpr Kv8Split kKv8SplitList{128, 8192};
+// soft votes: by the tokens that are there (lengths 16383, 1, 1000, 4097: 13.6 us, 17.1 us
+// split by the longest alone), B = 4, L = 131072: 109 us, in one wave 125 us
+constexpr Kv8Split kKv8SplitVotes{kVoteMinChunk, 2048};
 constexpr Kv8Split kKv8SplitF32{32, 2048};     // tokens one by one (B = 2, L = 512: 16.4 us with 128, 9.6 us with 32)
 inline long long kv8_round_chunk(long long chunk, const Kv8Split& how) {
   const long long unit = how.long_chunk > 4096 && chunk >= 4096 ? kAttnWarps * kKv8Seg : 32;

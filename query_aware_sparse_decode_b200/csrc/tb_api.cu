@@ -543,7 +543,10 @@ static tb_status launch_softvote(tb_ctx* ctx, int layer, const void* q, float* v
   p.Hkv = c.n_kv_heads;
   p.max_len = c.max_len;
   p.nchunk = (c.max_len + kVoteMinChunk - 1) / kVoteMinChunk;
-  {  // about four CTAs per SM in one wave, whatever B and L
+  if (ls.kv8) {
+    int nsplit = 0;
+    attn_split_kv8(ctx->num_sms, c.n_kv_heads, ls.lens, c.batch, p.nchunk, kKv8SplitVotes, &p.chunk, &nsplit);
+  } else {  // about four CTAs per SM in one wave, whatever B and L
     const int nsplit = std::max(1, 4 * ctx->num_sms / (c.batch * c.n_kv_heads));
     const int chunk = ((maxL + nsplit - 1) / nsplit + 15) / 16 * 16;
     p.chunk = std::max(kVoteMinChunk, chunk);
