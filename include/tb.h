@@ -185,7 +185,10 @@ TB_API tb_status tb_bind_layer_paged(tb_ctx* ctx, int layer, void* k_pool, void*
  * tb_append_kv / tb_decode_step (one token) and tb_append_kv_rows, all of which
  * form K_imp from the unrounded keys, so that selections do not depend on the
  * cache's format; tb_project_kimp recomputes K_imp from the codes (fp32 FMA).
- * Every call works on such layers, and a context may mix them with others.
+ * Every call works on such layers, and a context may mix them with others.  In
+ * the attention over bf16 queries a token's weight (softmax numerator times V
+ * scale) keeps 11 bits down to 2^-25 of the largest of its head and vanishes
+ * below 2^-36 of it; sums are fp32.
  * Lengths start at 0. */
 #define TB_KV8_BLOCK 16
 typedef enum { TB_KV8_E4M3 = 1, TB_KV8_INT8 = 2 } tb_kv8_format;

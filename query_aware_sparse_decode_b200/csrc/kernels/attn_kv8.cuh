@@ -368,9 +368,9 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // Softmax (log2 domain, fp32): l sums p = 2^(x - T); the weights of the V codes
 // are w = 2^(x + log2 vs - R + 15) with a reference of their own, so that fp16
 // holds them whatever the blocks' scales are.  T and R are not the exact maxima
-// but 8 above one: they move only when a logit passes them (p <= 1, w <= 2^15),
+// but 4 above one: they move only when a logit passes them (p <= 1, w <= 2^15),
 // which after the first tiles is rare, and saves the cross-lane maximum of every
-// tile.  Weights keep fp16's 11 bits down to 2^-21 of the largest one.
+// tile.  Weights keep fp16's 11 bits down to 2^-25 of the largest one.
 template <int FMT, int D, int GS, bool DENSE>
 __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(const AttnKv8Params p) {
   pdl_wait();
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
 #pragma unroll
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   // of heads 2tq + {0,1}: the reference T (kNone: no token yet), T - R + 15, the lane's part of l
-  constexpr float kNone = -1e30f;
+  constexpr float kNone = -1e30f, kHead = 4.f;
   float ref[2] = {kNone, kNone}, lift[2] = {15.f, 15.f}, l_run[2] = {0.f, 0.f};
 
   // copies of a tile's 16 rows (of cache rows rows[r] = that of token c_row + CR r)
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
           rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, sh));
         }
         const float t_old = ref[e], r_old = t_old - lift[e] + 15.f;
-        const float t_new = mt > t_old ? mt + 8.f : t_old, r_new = rt > r_old ? rt + 8.f : r_old;
+        const float t_new = mt > t_old ? mt + kHead : t_old, r_new = rt > r_old ? rt + kHead : r_old;
         // a head with no token so far has l = 0 and o = 0: any factor serves
         if (t_new != t_old) l_run[e] *= fast_exp2(t_old - t_new);
         const float al = r_new != r_old ? fast_exp2(r_old - r_new) : 1.f;
