@@ -365,18 +365,23 @@ class Context:
         [B][Hkv][n][D] (kv_dtype), any strides with contiguous rows (a view
         of a fused projection's output serves); counts: n for all by default."""
         B, H, D = self._rows
-        if k.dim() != 4 or k.shape != v.shape:
-            raise ValueError(f"k and v must be [B][Hkv][n][D] alike, got {tuple(k.shape)} and {tuple(v.shape)}")
-        n = k.shape[2]
+        shape = k.shape
+        if len(shape) != 4 or v.shape != shape:
+            raise ValueError(f"k and v must be [B][Hkv][n][D] alike, got {tuple(shape)} and {tuple(v.shape)}")
+        n = shape[2]
         self._expect("k", k, (B, H, n, D), self._kv_dtype)
-        self._expect("v", v, (B, H, n, D), self._kv_dtype)
-        counts = [n] * B if counts is None else [int(x) for x in counts]
-        if len(counts) != B or min(counts) < 0 or max(counts) > n:
-            raise ValueError(f"counts must be {B} numbers in [0, {n}], got {counts}")
+        if v.dtype != k.dtype or v.get_device() != self._index:
+            self._expect("v", v, shape, self._kv_dtype)
+        if counts is None:
+            counts = [n] * B
+        elif len(counts) != B or min(counts) < 0 or max(counts) > n:
+            raise ValueError(f"counts must be {B} numbers in [0, {n}], got {list(counts)}")
         if n == 0:
             return
-        self._on_device("tb_append_kv_rows", stream, layer, k.data_ptr(), v.data_ptr(), _row_strides("k", k),
-                        _row_strides("v", v), self._lens_type(*counts))
+        ks = _row_strides("k", k)
+        vs = ks if v.stride() == k.stride() else _row_strides("v", v)
+        self._on_device("tb_append_kv_rows", stream, layer, k.data_ptr(), v.data_ptr(), ks, vs,
+                        self._lens_type(*map(int, counts)))
 
     def read_kv(self, layer: int, start: int, count: int, k_out=None, v_out=None, stream=None) -> None:
         """Rows [start, start + count) of an 8-bit layer as values into k_out
