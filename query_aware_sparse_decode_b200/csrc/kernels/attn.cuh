@@ -44,16 +44,16 @@ struct AttnParams {
   int lens[kMaxBatch];
 };
 
-// Lists the union tokens of [t0, t1) (at most MAXC tokens, MAXC / 32 mask
+// Lists the union tokens of [t0, t1) (at most kAttnMaxChunk tokens, 64 mask
 // words) in ascending order: put(position, token, head bits) for each, and up
-// to a multiple of PAD positions put(position, t0, 0).  Returns their number
+// to a multiple of 16 positions put(position, t0, 0).  Returns their number
 // (without the padding).  Warps 0 and 1 read the words (one per lane) and scan
 // their counts; then each thread expands half a word (16 tokens).
-template <int GS, int MAXC, int PAD, class Put>
+template <int GS, class Put>
 __device__ __forceinline__ int build_union(const AttnParams& p, int b, int g, int t0, int t1, uint32_t* scan_sm,
                                            Put put) {
-  constexpr int NWM = MAXC / 32;
-  static_assert(NWM <= 64 && kAttnThreads >= 2 * NWM, "two warps hold the words; a thread expands half a word");
+  constexpr int NWM = kAttnMaxChunk / 32;
+  static_assert(NWM <= 64 && kAttnThreads == 2 * NWM, "two warps hold the words; a thread expands half a word");
   __shared__ uint32_t s_u[NWM], s_excl[NWM], s_hm[GS][NWM];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nwords = (t1 - t0 + 31) >> 5;
@@ -116,7 +116,7 @@ __device__ __forceinline__ int build_union(const AttnParams& p, int b, int g, in
       }
     }
   }
-  const int padded = (total + PAD - 1) / PAD * PAD;
+  const int padded = (total + kAttnTile - 1) / kAttnTile * kAttnTile;
   for (int i = total + tid; i < padded; i += kAttnThreads) put(i, t0, 0u);
   __syncthreads();
   return total;
@@ -126,7 +126,7 @@ __device__ __forceinline__ int build_union(const AttnParams& p, int b, int g, in
 template <int GS>
 __device__ __forceinline__ int build_union_list(const AttnParams& p, int b, int g, int t0, int t1, int32_t* list_idx,
                                                 uint8_t* list_hb, uint32_t* scan_sm) {
-  return build_union<GS, kAttnMaxChunk, kAttnTile>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
+  return build_union<GS>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
     list_idx[pos] = (int32_t)kv_row(p.kl, b, g, p.Hkv, p.max_len, t);
     list_hb[pos] = (uint8_t)hb;
   });

@@ -87,7 +87,7 @@ constexpr int attn_kv8_f32_smem() { return kKv8ListBytes + kAttnWarps * GS * (D 
 template <int GS>
 __device__ __forceinline__ int build_union_list_kv8(const AttnKv8Params& p, int b, int g, int t0, int t1,
                                                     int32_t* list_idx, uint8_t* list_hb, uint32_t* scan_sm) {
-  return build_union<GS, kAttnMaxChunk, kAttnTile>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
+  return build_union<GS>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
     uint32_t row;
     if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &row)) {
       atomicOr(p.status, TB_DEV_ERR_INDEX);
@@ -371,6 +371,11 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // but 4 above one: they move only when a logit passes them (p <= 1, w <= 2^15),
 // which after the first tiles is rare, and saves the cross-lane maximum of every
 // tile.  Weights keep fp16's 11 bits down to 2^-25 of the largest one.
+//
+// Measured with the combine (32 / 8 heads, D = 128, e4m3, L = 131072, B = 4): every
+// token 166 us, 6.5 TB/s, the copy peak; 30 % per head 132 us, 6.2 TB/s (gathered 128-byte
+// rows); one set of 30 % per KV group 62 us, 5.2 TB/s.  int8 takes 3 to 10 % longer (454
+// instructions a tile against 357: its widening has no instruction of its own).
 template <int FMT, int D, int GS, bool DENSE>
 __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(const AttnKv8Params p) {
   pdl_wait();
@@ -742,7 +747,8 @@ struct VoteKv8Params : VoteParams {
 // Soft-vote logits (log2 domain) and per-chunk (max, sum) pairs over 8-bit
 // keys; softvote_reduce_kernel follows.  S^T = K Q^T as in attn_kv8_kernel, over
 // consecutive tokens: a tile of 16 is one block of the cache, so it has one
-// scale and one row lookup.  A ring of kVoteKv8Stages tiles per warp.
+// scale and one row lookup.  A ring of kVoteKv8Stages tiles per warp.  Measured (B = 1, L =
+// 131072): 25 us of the call's 34 us, 5.3 TB/s, over half of the issue slots used.
 constexpr int kVoteKv8Stages = 3;
 template <int D>
 constexpr int vote_kv8_smem() { return kVoteWarps * kVoteKv8Stages * (kAttnTile * D + 16); }
