@@ -16,7 +16,42 @@ namespace tb {
 struct AttnKv8Params : AttnParams {
   const float* k_scale;  // one per 16 cache rows
   const float* v_scale;
+  // calls of one split: the output itself (bf16 or fp32) and its lse, no combine (out null: partials)
+  void* out;             // [B][Hq][D]
+  float* lse;            // [B][Hq] or null
+  int out_bf16;
 };
+
+// The heads' outputs from the CTA's per-warp states in shared memory (wm null: a
+// sequence without tokens): what write_partial and the combine kernel make of a single
+// split, without their traffic and launch (128 sequences, dense: of 512 tokens 41.5 -> 29.9
+// us, of 100 24.6 -> 12.7 us).
+template <int D, int GS>
+__device__ __forceinline__ void write_output(const AttnKv8Params& p, int b, int g, const float* wm, const float* wl,
+                                             const float* wo) {
+  for (int e = threadIdx.x; e < GS * D; e += kAttnThreads) {
+    const int hh = e / D, d = e % D;
+    float M = kNegInf, o = 0.f, l = 0.f;
+    if (wm != nullptr) {
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, wm[w * GS + hh]);
+    }
+    if (M != kNegInf) {
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float m = wm[w * GS + hh];
+        const float f = m == kNegInf ? 0.f : exp2f(m - M);
+        o += f * wo[(w * GS + hh) * D + d];
+        l += f * wl[w * GS + hh];
+      }
+      o *= 1.f / l;
+    }
+    const size_t row = (size_t)b * p.Hq + g * GS + hh;
+    if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[row * D + d] = __float2bfloat16_rn(o);
+    else reinterpret_cast<float*>(p.out)[row * D + d] = o;
+    if (p.lse != nullptr && d == 0) p.lse[row] = M == kNegInf ? kNegInf : (M + log2f(l)) * 0.69314718055994531f;
+  }
+}
 
 // Split of the 8-bit attention (host side), counting the tokens that each
 // sequence has: the shortest chunks (whole mask words) that keep the call's CTAs
@@ -127,7 +162,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kv8_f32_kernel(const AttnKv
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int L = p.lens[b];
   const int t0 = split * p.chunk;
-  if (t0 >= L) return;
+  if (t0 >= L) {
+    if (p.out != nullptr) write_output<D, GS>(p, b, g, nullptr, nullptr, nullptr);
+    return;
+  }
   const int t1 = min(t0 + p.chunk, L);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint8_t* Kb = reinterpret_cast<const uint8_t*>(p.k_cache) + lane * DPL;
@@ -191,7 +229,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kv8_f32_kernel(const AttnKv
     for (int j = 0; j < DPL; ++j) wo[(warp * GS + hh) * D + lane * DPL + j] = o[hh][j];
   }
   __syncthreads();
-  write_partial<D, GS>(p, b, g, split, wm, wl, wo);
+  if (p.out != nullptr) write_output<D, GS>(p, b, g, wm, wl, wo);
+  else write_partial<D, GS>(p, b, g, split, wm, wl, wo);
 }
 
 // ---------------------------------------------------------------- tensor cores
@@ -390,7 +429,10 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int L = p.lens[b];
   const int t0 = split * p.chunk;
-  if (t0 >= L) return;
+  if (t0 >= L) {
+    if (p.out != nullptr) write_output<D, GS>(p, b, g, nullptr, nullptr, nullptr);
+    return;
+  }
   const int t1 = min(t0 + p.chunk, L);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = lane >> 2, tq = lane & 3;
@@ -736,7 +778,8 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     }
   }
   __syncthreads();
-  write_partial<D, GS>(p, b, g, split, wm, wl, wo);
+  if (p.out != nullptr) write_output<D, GS>(p, b, g, wm, wl, wo);
+  else write_partial<D, GS>(p, b, g, split, wm, wl, wo);
 }
 
 struct VoteKv8Params : VoteParams {

@@ -399,7 +399,8 @@ static tb_status launch_select(tb_ctx* ctx, int layer, const float* scores, bool
   return s;
 }
 
-// The split attention kernel over an 8-bit layer (the partials' combine is the caller's).
+// The split attention kernel over an 8-bit layer: into `out` and `lse` (a call of one
+// split), or with `out` null into the partials, whose combine is the caller's.
 template <int F, int D, int GS>
 static tb_status launch_attn_kv8_as(bool bf16, const AttnKv8Params& p, dim3 grid, cudaStream_t st) {
   const bool dense = p.mask_mode == TB_MASK_DENSE;
@@ -412,14 +413,17 @@ static tb_status launch_attn_kv8_as(bool bf16, const AttnKv8Params& p, dim3 grid
   launch_pdl(k, grid, dim3(kAttnThreads), smem, st, p);
   return cuda_status(cudaGetLastError());
 }
-static tb_status launch_attn_kv8(const tb_ctx* ctx, const LayerState& ls, const AttnParams& base, dim3 grid,
-                                 cudaStream_t st) {
+static tb_status launch_attn_kv8(const tb_ctx* ctx, const LayerState& ls, const AttnParams& base, void* out, float* lse,
+                                 bool out_bf16, dim3 grid, cudaStream_t st) {
   const tb_config& c = ctx->cfg;
   const int gs = c.n_q_heads / c.n_kv_heads;
   AttnKv8Params p{};
   static_cast<AttnParams&>(p) = base;
   p.k_scale = ls.k_scale;
   p.v_scale = ls.v_scale;
+  p.out = out;
+  p.lse = lse;
+  p.out_bf16 = out_bf16;
 #define TB_KV8_CASE(F, DV, GSV) \
   if (ls.kv8 == F && c.head_dim == DV && gs == GSV) return launch_attn_kv8_as<F, DV, GSV>(c.kv_dtype == TB_BF16, p, grid, st);
 #define TB_KV8_CASES(F)                                                                           \
@@ -465,8 +469,15 @@ static tb_status launch_attn(tb_ctx* ctx, int layer, const void* q, const uint32
   {
     dim3 grid(p.nsplit, c.n_kv_heads, c.batch);
     if (ls.kv8) {
-      const tb_status s8 = launch_attn_kv8(ctx, ls, p, grid, st);
+      const bool whole = p.nsplit == 1;
+      const tb_status s8 = launch_attn_kv8(ctx, ls, p, whole ? out : nullptr, lse, c.kv_dtype == TB_BF16 && !out_f32, grid, st);
       if (s8 != TB_OK) return s8;
+      if (whole) {
+        ++ctx->launches;
+        trace_point(ctx, 4, st);
+        trace_point(ctx, 5, st);
+        return TB_OK;
+      }
     } else
 #define TB_ATTN_CASE(DV, GSV)                                                                               \
   if (c.head_dim == DV && gs == GSV) {                                                                      \

@@ -366,6 +366,22 @@ def test_attention_lengths(fmt, L):
         c.check_attention(q, sets, out, lse, f"{mode} L{L}")
 
 
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("int8", "bf16"), ("e4m3", "f32")])
+def test_large_batches(fmt, dtype):
+    """More (sequence, KV head) pairs than CTAs of a wave: one split each, sequences
+    without a token among them."""
+    c = Case(fmt, dtype, B=80, Hq=16, Hkv=8, D=64, dimp=16, max_len=256, seed=80)
+    c.append([int(x) for x in c.rng.choice([0, 1, 15, 33, 100, 250], size=80)])
+    for mode in ("head", "shared", "dense"):
+        q, mask, sets, out, lse = run_attention(c, mode, empty={(2, 0)} if mode != "dense" else ())
+        c.check_attention(q, sets, out, lse, mode)
+        part = torch.zeros(c.B * c.Hq * (c.D + 1), device="cuda")
+        c.ctx.sparse_attn_partial(0, q, mask, MODES[mode], part)
+        torch.cuda.synchronize()
+        n = c.B * c.Hq * c.D
+        assert torch.equal(part[:n].view_as(out).to(out.dtype), out) and torch.equal(part[n:].view_as(lse), lse)
+
+
 @pytest.mark.parametrize("spread", [20, 60])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_attention_over_blocks_of_very_different_scale(fmt, spread):
