@@ -342,8 +342,9 @@ constexpr int attn_kv8_smem() {
   constexpr int merge = kAttnWarps * GS * (D + 2) * 4;
   return work > merge ? work : merge;
 }
-// log2 of a V scale; finite or -inf, so that a masked token's weight stays zero over any scale
-__device__ __forceinline__ float kv8_log2_scale(float vs) { return fminf(__log2f(vs), 1e30f); }
+// log2 of a V scale, in [-200, 200], which holds every positive finite one; a scale of zero (a
+// block never written) weighs 2^-200
+__device__ __forceinline__ float kv8_log2_scale(float vs) { return fminf(fmaxf(__log2f(vs), -200.f), 200.f); }
 // 16-byte pieces of a cached row are stored at piece ^ swizzle(row), so that the
 // lanes of a shared-memory phase touch different banks: for K two rows' pieces
 // tq, for V rows 0, 2, 4, 6 (+ 1) of two neighbouring pieces.  Both are linear over
@@ -410,6 +411,10 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // but 4 above one: they move only when a logit passes them (p <= 1, w <= 2^15),
 // which after the first tiles is rare, and saves the cross-lane maximum of every
 // tile.  Weights keep fp16's 11 bits down to 2^-25 of the largest one.
+// References and exponents come from one rounded x, and R is held as its distance
+// from T: however large the logits are, x - T is exact where it matters and not above
+// 0, and log2 vs is added to it and not to x.  (From the unrounded product a weight
+// passed fp16 above |x| = 2^26 or so, where the step of x exceeds the 4.)
 //
 // Measured with the combine (32 / 8 heads, D = 128, e4m3, L = 131072, B = 4): every
 // token 166 us, 6.5 TB/s, the copy peak; 30 % per head 132 us, 6.2 TB/s (gathered 128-byte
@@ -458,9 +463,9 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
   float o[MT][4];  // dims grp D/8 + 2mt (+1), heads 2tq + {0,1}
 #pragma unroll
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  // of heads 2tq + {0,1}: the reference T (kNone: no token yet), T - R + 15, the lane's part of l
-  constexpr float kNone = -1e30f, kHead = 4.f;
-  float ref[2] = {kNone, kNone}, lift[2] = {15.f, 15.f}, l_run[2] = {0.f, 0.f};
+  // of heads 2tq + {0,1}: the reference T (kLowest: no token yet), T - R + 15, the lane's part of l
+  constexpr float kLowest = -3.402823466e38f, kHead = 4.f;
+  float ref[2] = {kLowest, kLowest}, lift[2] = {15.f, 15.f}, l_run[2] = {0.f, 0.f};
 
   // copies of a tile's 16 rows (of cache rows rows[r] = that of token c_row + CR r)
   auto copy_rows = [&](uint32_t off, const uint32_t (&rows)[kAttnTile / CR]) {
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
       }
       kv8_scores<FMT, D>(ka, kb, qb, s);
     }
-    // x = s f; d = x - T; z = d + log2 vs + T - R + 15
+    // x = s f, rounded once; d = x - T; z = d + log2 vs + T - R + 15
     float f[2][2], ev[2];
     uint32_t hb[2];  // tokens grp and grp + 8: their heads
     bool masked = true;
@@ -674,6 +679,8 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
         hb[r] = e.z;
       }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = __fmul_rn(s[j], f[j >> 1][j & 1]);  // x (never fused into d)
     float d[4], z[4];
     auto exponents = [&]() {
 #pragma unroll
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int j = 2 * r + e;
-          d[j] = fmaf(s[j], f[r][e], -ref[e]);
+          d[j] = s[j] - ref[e];
           if (masked && !(hb[r] & head_bit[e])) d[j] = kNegInf;
           z[j] = d[j] + (ev[r] + lift[e]);
         }
@@ -691,25 +698,24 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     if (__any_sync(0xffffffffu, dm > 0.f || zm > 15.f)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mt = kNegInf, rt = kNegInf;  // the tile's largest x and x + log2 vs of the head
+        float mt = kNegInf, rt = kNegInf;  // the head's largest x, and x - T + log2 vs, of the tile
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          if (!masked || (hb[r] & head_bit[e])) {
-            mt = fmaxf(mt, s[2 * r + e] * f[r][e]);
-            rt = fmaxf(rt, s[2 * r + e] * f[r][e] + ev[r]);
-          }
+          if (!masked || (hb[r] & head_bit[e])) mt = fmaxf(mt, s[2 * r + e]);
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) {
-          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, sh));
-          rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, sh));
-        }
-        const float t_old = ref[e], r_old = t_old - lift[e] + 15.f;
-        const float t_new = mt > t_old ? mt + kHead : t_old, r_new = rt > r_old ? rt + kHead : r_old;
-        // a head with no token so far has l = 0 and o = 0: any factor serves
+        for (int sh = 4; sh < 32; sh <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, sh));
+        const float t_old = ref[e], t_new = mt > t_old ? mt + kHead : t_old;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (!masked || (hb[r] & head_bit[e])) rt = fmaxf(rt, (s[2 * r + e] - t_new) + ev[r]);
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, sh));
+        // R - T, before and after (a head with no token so far has l = 0 and o = 0: any factor serves)
+        const float r_old = (15.f - lift[e]) - (t_new - t_old), r_new = rt > r_old ? rt + kHead : r_old;
         if (t_new != t_old) l_run[e] *= fast_exp2(t_old - t_new);
         const float al = r_new != r_old ? fast_exp2(r_old - r_new) : 1.f;
         ref[e] = t_new;
-        lift[e] = t_new - r_new + 15.f;
+        lift[e] = 15.f - r_new;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
           o[j][e] *= al;
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
     const int h = 2 * tq + e;
     if (h < GS) {
       if (grp == 0) {
-        wm[warp * GS + h] = ref[e] == kNone && l_run[e] == 0.f ? kNegInf : ref[e];  // (a NaN logit moves no reference)
+        wm[warp * GS + h] = l_run[e] == 0.f ? kNegInf : ref[e];  // no token (a NaN logit moves no reference)
         wl[warp * GS + h] = l_run[e];
       }
       const float f = exp2f(-lift[e]);  // back from the weights' reference to T
@@ -847,7 +853,8 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
   const int hp = 2 * tq;
   const bool real[2] = {hp < GS, hp + 1 < GS};
   // per lane and head: a reference (8 above a logit that passed the last one) and the sum of 2^(x - it)
-  float m[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f};
+  constexpr float kLowest = -3.402823466e38f;
+  float m[2] = {kLowest, kLowest}, l[2] = {0.f, 0.f};
   float* lrow[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
@@ -874,8 +881,8 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float f = qs[e] * (ks * p.scale_log2);
-      x[e] = s[e] * f;
-      x[2 + e] = s[2 + e] * f;
+      x[e] = __fmul_rn(s[e], f);  // rounded once: the reduce pass reads these logits
+      x[2 + e] = __fmul_rn(s[2 + e], f);
     }
     const bool in[2] = {grp < left, grp + 8 < left};
     if (left < kAttnTile || !(ks == ks)) {
@@ -898,7 +905,7 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
   }
 #pragma unroll
   for (int e = 0; e < 2; ++e)
-    if (m[e] == -1e30f) m[e] = kNegInf;  // no token
+    if (l[e] == 0.f) m[e] = kNegInf;  // no token
   cp_async_wait<0>();
   // merge the lanes' pairs of each head (the 8 lanes with the same tq)
 #pragma unroll

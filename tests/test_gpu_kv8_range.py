@@ -1,0 +1,78 @@
+"""Attention and votes over 8-bit caches at the ends of the range: logits far past fp32's integers, tokens that
+tie there, all logits far below zero."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8 as O8
+from query_aware_sparse_decode_b200 import tb as TB
+
+from harness import mask_from_sets
+from test_gpu_kv8 import DT, MODES, Case, dev, host, random_sets
+
+pytestmark = pytest.mark.gpu
+
+
+def one_hot_case(fmt, dtype, up, sign, L=(700, 90)):
+    """Logits without any rounding before the scale: query h has one element, +-1 at dim h, and the keys hold j 2^up
+    (j one of 64, 72 .. 120: four significant bits, exact in both formats) there.  V blocks differ by up to 2^24."""
+    gs = 4
+    c = Case(fmt, dtype, B=2, Hq=8, Hkv=2, D=128 if dtype == "bf16" else 64, max_len=768, seed=up)
+    n = max(L)
+    k = np.zeros((2, 2, n, c.D))
+    k[..., :gs] = sign * c.rng.integers(8, 16, size=(2, 2, n, gs)) * 8.0 * 2.0 ** up
+    v = c.rng.normal(size=k.shape) * np.exp2(np.repeat(c.rng.integers(-12, 12, size=(n + 15) // 16), 16)[:n])[:, None]
+    c.append(L, k=k, v=v)
+    q = np.zeros((2, 8, c.D))
+    for h in range(8):
+        q[:, h, h % gs] = 1.0 if h < 6 or sign < 0 else -1.0
+    return c, q
+
+
+@pytest.mark.parametrize("mode", ["head", "dense"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("up", [4, 13, 20, 27, 40, 100])
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("int8", "bf16"), ("e4m3", "f32"), ("int8", "f32")])
+def test_attention_with_large_logits(fmt, dtype, up, sign, mode):
+    """Equal keys have equal logits, bit for bit, and others are at least 2^up apart: the softmax is even over the
+    largest ones, and its error is that of the weights (fp16: half a step, 2^-11) and of the output's type."""
+    c, q = one_hot_case(fmt, dtype, up, sign)
+    sets, mask = c.all_tokens(), None
+    if mode == "head":
+        sets = random_sets(c, c.Hq, 0.3, empty={(1, 2)})
+        mask = mask_from_sets(sets, c.B, c.Hq, c.max_len)
+    out = torch.full((c.B, c.Hq, c.D), 9.0, dtype=DT[dtype], device="cuda")
+    lse = torch.full((c.B, c.Hq), 9.0, device="cuda")
+    c.ctx.sparse_attn(0, dev(q, dtype), mask, MODES[mode], out, lse)
+    torch.cuda.synchronize()
+    assert c.ctx.check_status() == 0
+    half, w = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 0.0)
+    for b in range(c.B):
+        for h in range(c.Hq):
+            o, z, weight, _ = O8.attend(q[b, h], c.val["k"][b, h // c.gs], c.val["v"][b, h // c.gs], sets[b, h])
+            # z's terms: the product with log2e / sqrt(D) and its own rounding, log2 and the way back, half a step each
+            assert float(lse[b, h]) == z if z == -math.inf else abs(float(lse[b, h]) - z) <= 8 * 2.0 ** -24 * abs(z) + 2e-6
+            tol = half * np.abs(o) + (w + 1e-5) * weight + 1e-36
+            assert np.all(np.abs(host(out)[b, h] - o) <= tol), f"b{b} h{h}"
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("up", [4, 20, 27, 40, 100])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_votes_with_large_logits(fmt, up, sign):
+    c, q = one_hot_case(fmt, "bf16", up, sign)
+    votes = torch.full((c.B, c.max_len), 3.0, device="cuda")
+    c.ctx.softvote_scores(0, dev(q, "bf16"), votes)
+    torch.cuda.synchronize()
+    for b, L in enumerate(c.lens):
+        ref, slack = np.zeros(L), np.zeros(L)
+        for h in range(c.Hq):
+            a = c.val["k"][b, h // c.gs, :L] @ q[b, h] / math.sqrt(c.D)
+            p = np.exp(a - a.max())
+            ref += p / p.sum()
+            # a logit below the largest: three roundings (log2e / sqrt(D), its product with the scale, the logit) of
+            # each of the two, half a step 2^-24 each, move their distance; equal ones move together
+            slack += np.where(a < a.max(), p / p.sum() * 6 * 2.0 ** -24 * np.abs(a).max(), 0.0)
+        assert np.all(np.abs(host(votes)[b, :L] - ref) <= 4e-6 * ref + slack + 1e-30), f"b{b}"
