@@ -655,16 +655,16 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
       }
       kv8_scores<FMT, D>(ka, kb, qb, s);
     }
-    // x = s f, rounded once; d = x - T; z = d + log2 vs + T - R + 15
-    float f[2][2], ev[2];
+    // x = (s qs) f, rounded once (s qs is exact above 2^-102, and in range where qs f need not be); d = x - T;
+    // z = d + log2 vs + T - R + 15
+    float f[2], ev[2];
     uint32_t hb[2];  // tokens grp and grp + 8: their heads
     bool masked = true;
     if constexpr (DENSE) {
       const uint2 sc = lds8(meta + stage * (kAttnTile * 16));
       const float ks = __uint_as_float(sc.x);
       ev[0] = ev[1] = kv8_log2_scale(__uint_as_float(sc.y));
-#pragma unroll
-      for (int e = 0; e < 2; ++e) f[0][e] = f[1][e] = qs[e] * (ks * p.scale_log2);
+      f[0] = f[1] = ks * p.scale_log2;
       const int left = ks == ks ? t1 - t0 - (warp + it * kAttnWarps) * kAttnTile : 0;
       masked = left < kAttnTile;
       hb[0] = grp < left ? ~0u : 0u;
@@ -674,13 +674,12 @@ __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(c
       for (int r = 0; r < 2; ++r) {
         const uint4 e = lds16(meta + (stage * kAttnTile + grp + 8 * r) * 16);
         ev[r] = __uint_as_float(e.y);
-        f[r][0] = qs[0] * __uint_as_float(e.x);
-        f[r][1] = qs[1] * __uint_as_float(e.x);
+        f[r] = __uint_as_float(e.x);
         hb[r] = e.z;
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = __fmul_rn(s[j], f[j >> 1][j & 1]);  // x (never fused into d)
+    for (int j = 0; j < 4; ++j) s[j] = __fmul_rn(s[j] * qs[j & 1], f[j >> 1]);  // x (never fused into d)
     float d[4], z[4];
     auto exponents = [&]() {
 #pragma unroll
@@ -877,13 +876,10 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
     kv8_scores<FMT, D>(ka, kb, qb, s);
     const float ks = __uint_as_float(lds8(scales + 16 * stage).x);
     const int left = t1 - t0 - (warp + it * kVoteWarps) * kAttnTile;
+    const float f = ks * p.scale_log2;
     float x[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float f = qs[e] * (ks * p.scale_log2);
-      x[e] = __fmul_rn(s[e], f);  // rounded once: the reduce pass reads these logits
-      x[2 + e] = __fmul_rn(s[2 + e], f);
-    }
+    for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(s[j] * qs[j & 1], f);  // rounded once: the reduce pass reads these logits
     const bool in[2] = {grp < left, grp + 8 < left};
     if (left < kAttnTile || !(ks == ks)) {
 #pragma unroll

@@ -76,3 +76,37 @@ def test_votes_with_large_logits(fmt, up, sign):
             # each of the two, half a step 2^-24 each, move their distance; equal ones move together
             slack += np.where(a < a.max(), p / p.sum() * 6 * 2.0 ** -24 * np.abs(a).max(), 0.0)
         assert np.all(np.abs(host(votes)[b, :L] - ref) <= 4e-6 * ref + slack + 1e-30), f"b{b}"
+
+
+@pytest.mark.parametrize("mode", ["head", "dense"])
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("int8", "bf16"), ("e4m3", "f32")])
+def test_large_queries_beside_large_scales(fmt, dtype, mode):
+    """Keys with 2^120 in a dimension that the queries, 2^60 elsewhere, do not read: the products are zero in those
+    blocks and ordinary in the others, though query times scale passes fp32."""
+    c = Case(fmt, dtype, B=1, Hq=4, Hkv=1, D=64, max_len=256, seed=7)
+    k = c.rng.normal(size=(1, 1, 90, 64)) * 2.0 ** -60
+    k[0, 0, [20, 70], 5] = 2.0 ** 120, -1.5 * 2.0 ** 119
+    c.append([90], k=k, v=c.rng.normal(size=k.shape))
+    q = c.rng.normal(size=(1, 4, 64)) * 2.0 ** 60
+    q[..., 5] = 0.0
+    q = dev(q, dtype)
+    sets, mask = c.all_tokens(), None
+    if mode == "head":
+        sets = random_sets(c, c.Hq, 0.5)
+        mask = mask_from_sets(sets, 1, c.Hq, c.max_len)
+    out, lse = torch.zeros((1, 4, 64), dtype=DT[dtype], device="cuda"), torch.zeros((1, 4), device="cuda")
+    c.ctx.sparse_attn(0, q, mask, MODES[mode], out, lse)
+    votes = torch.zeros((1, 256), device="cuda")
+    if dtype == "bf16":
+        c.ctx.softvote_scores(0, q, votes)
+    torch.cuda.synchronize()
+    assert c.ctx.check_status() == 0
+    c.check_attention(q, sets, out, lse)
+    if dtype == "bf16":
+        ref, slack = np.zeros(90), 0.0
+        for h in range(4):
+            a = c.val["k"][0, 0, :90] @ host(q)[0, h] / 8.0
+            p = np.exp(a - a.max())
+            ref += p / p.sum()
+            slack = max(slack, 72 * 2.0 ** -24 * float((np.abs(c.val["k"][0, 0, :90]) @ np.abs(host(q)[0, h])).max()) / 8.0)
+        assert np.all(np.abs(host(votes)[0, :90] - ref) <= (2 * slack + 4e-6) * ref + 1e-30)
