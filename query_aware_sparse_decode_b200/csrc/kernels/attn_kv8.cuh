@@ -928,9 +928,12 @@ __global__ void __launch_bounds__(kVoteThreads, 4) softvote_kv8_logits_kernel(co
     if (M != kNegInf)
       for (int w = 0; w < kVoteWarps; ++w)
         if (wm[w * GS + tid] != kNegInf) sum += wl[w * GS + tid] * exp2f(wm[w * GS + tid] - M);
+    // A chunk whose pages are all outside the pool counts as one token of the lowest logit: nothing
+    // beside other chunks, and a sum to divide by where there are none (its logits of -inf vote 0).
+    const bool none = M == kNegInf;
     const size_t ph = (((size_t)b * p.Hq + g * GS + tid) * p.nchunk + chunk) * 2;
-    p.stats[ph] = M;
-    p.stats[ph + 1] = sum;
+    p.stats[ph] = none ? kLowest : M;
+    p.stats[ph + 1] = none ? 1.f : sum;
   }
 }
 
