@@ -118,14 +118,15 @@ constexpr int attn_kv8_f32_smem() { return kKv8ListBytes + kAttnWarps * GS * (D 
 
 // The gather list of a sub-chunk, page ids checked: a token whose page is not
 // one of the pool's is listed without a head (nothing reads its codes as a
-// selected row) and flags TB_DEV_ERR_INDEX.
+// selected row) and flags TB_DEV_ERR_INDEX.  The list's padding (no head either)
+// flags nothing: its token need not be one of the union's.
 template <int GS>
 __device__ __forceinline__ int build_union_list_kv8(const AttnKv8Params& p, int b, int g, int t0, int t1,
                                                     int32_t* list_idx, uint8_t* list_hb, uint32_t* scan_sm) {
   return build_union<GS>(p, b, g, t0, t1, scan_sm, [&](int pos, int t, uint32_t hb) {
     uint32_t row;
     if (!kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t, &row)) {
-      atomicOr(p.status, TB_DEV_ERR_INDEX);
+      if (hb) atomicOr(p.status, TB_DEV_ERR_INDEX);
       hb = 0u;
     }
     list_idx[pos] = (int32_t)row;

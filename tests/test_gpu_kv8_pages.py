@@ -1,4 +1,4 @@
-"""Page ids outside the pool of an 8-bit layer: sequences with no other pages."""
+"""Page ids outside the pool of an 8-bit layer: sequences with no other pages, and pages that a call does not need."""
 import math
 
 import numpy as np
@@ -7,8 +7,8 @@ import torch
 
 from query_aware_sparse_decode_b200 import tb as TB
 
-from harness import sets_from_mask
-from test_gpu_kv8 import Case, dev
+from harness import mask_from_sets, sets_from_mask
+from test_gpu_kv8 import DT, MODES, Case, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,23 @@ def test_a_votes_step_over_a_sequence_without_pages_selects_in_order():
     assert c.ctx.check_status() == 1 and bool((out == 0).all())
     # 901 tokens: a sink of 4, a window of 16, 30 % of 901 = 270 of those between
     assert np.array_equal(sets_from_mask(mask, [901])[0, 0], np.concatenate([np.arange(274), np.arange(885, 901)]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pages_that_hold_no_listed_token_are_not_missed(dtype):
+    """One page after another leaves the pool; the mask lists tokens of the others only."""
+    c = Case("e4m3", dtype, B=1, D=64, page=16, max_len=256)
+    c.append((100,))
+    torch.cuda.synchronize()
+    for bad in range(4):
+        good = c.table.clone()
+        c.table[0, bad] = -1
+        sets = {(0, h): np.setdiff1d(np.arange(3, 90, 5), np.arange(16 * bad, 16 * bad + 16)) for h in range(c.Hq)}
+        mask = mask_from_sets(sets, 1, c.Hq, c.max_len)
+        q = dev(c.rng.normal(size=(1, c.Hq, c.D)), dtype)
+        out, lse = torch.zeros((1, c.Hq, c.D), dtype=DT[dtype], device="cuda"), torch.zeros((1, c.Hq), device="cuda")
+        c.ctx.sparse_attn(0, q, mask, MODES["head"], out, lse)
+        torch.cuda.synchronize()
+        assert c.ctx.check_status() == 0
+        c.check_attention(q, sets, out, lse, f"page {bad}")
+        c.table.copy_(good)
