@@ -200,8 +200,10 @@ TB_API tb_status tb_bind_layer_kv8(tb_ctx* ctx, int layer, int format, void* k_c
  * tb_bind_layer_paged (same limits).  A page's scales move with it.  A page
  * may be shared by sequences that only read it: the block a sequence appends
  * into must be its own.  A page id outside [0, num_pages) sets
- * TB_DEV_ERR_INDEX; its tokens are not written, not read back, left out of
- * the attention and the votes, and project to zero. */
+ * TB_DEV_ERR_INDEX where a call needs one of its tokens; these are not written,
+ * not read back, left out of the attention and the votes, and project to zero.
+ * Tokens past a sequence's length need no page (tb_project_kimp over a ragged
+ * batch: zeros, and no error). */
 TB_API tb_status tb_bind_layer_kv8_paged(tb_ctx* ctx, int layer, int format, void* k_pool, void* v_pool,
                                          float* k_scale, float* v_scale, int num_pages, const int32_t* page_table,
                                          int page_size, int max_pages, void* kimp_cache, const void* w_k);

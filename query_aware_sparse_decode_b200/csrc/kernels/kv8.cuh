@@ -496,10 +496,12 @@ struct Kv8ProjectParams {
   uint32_t* status;
   KvLayout kl;
   int Hkv, max_len, start, count, kimp_bf16;
+  int lens[kMaxBatch];
 };
 
 // K_imp of rows [start, start + count) from the cached (rounded) keys, fp32
-// FMA: grid (ceil(count/32), Hkv, B), 256 threads, 32 rows x d' outputs.
+// FMA: grid (ceil(count/32), Hkv, B), 256 threads, 32 rows x d' outputs.  A row without
+// a page projects to zero; it is missed (TB_DEV_ERR_INDEX) only below its sequence's length.
 template <typename T, int FMT, int D, int DIMP>
 __global__ void __launch_bounds__(256) kv8_project_kernel(const Kv8ProjectParams p) {
   constexpr int ROWS = 32;
@@ -513,18 +515,19 @@ __global__ void __launch_bounds__(256) kv8_project_kernel(const Kv8ProjectParams
   const int n = min(ROWS, p.start + p.count - t0);
   const T* W = reinterpret_cast<const T*>(p.w_k);
   for (int i = tid; i < D * DIMP; i += 256) ws[i / DIMP][i % DIMP] = to_f32(W[i]);
-  bool bad = false;
+  bool missed = false;
   if (tid < ROWS) {
     uint32_t row = 0;
     float s = 0.f;
     if (tid < n) {
-      bad = !kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t0 + tid, &row);
-      s = bad ? 0.f : p.scale[row >> 4];  // a row without a page projects to zero
+      const bool ok = kv_row_checked(p.kl, b, g, p.Hkv, p.max_len, t0 + tid, &row);
+      s = ok ? p.scale[row >> 4] : 0.f;
+      missed = !ok && t0 + tid < p.lens[b];
     }
     krow[tid] = row;
     kscale[tid] = s;
   }
-  if (__syncthreads_or(bad) && tid == 0) atomicOr(p.status, TB_DEV_ERR_INDEX);
+  if (__syncthreads_or(missed) && tid == 0) atomicOr(p.status, TB_DEV_ERR_INDEX);
   for (int i = tid; i < ROWS * D / 4; i += 256) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     float x[4];

@@ -1031,8 +1031,9 @@ TB_API tb_status tb_append_kv(tb_ctx* ctx, int layer, const void* k_new, const v
 static tb_status launch_kv8_project(tb_ctx* ctx, int layer, int start, int count, cudaStream_t st) {
   const tb_config& c = ctx->cfg;
   const LayerState& ls = ctx->layers[layer];
-  const Kv8ProjectParams p{static_cast<const uint8_t*>(ls.k), ls.k_scale, ls.kimp, ls.wk, ctx->status, ls.kl,
-                           c.n_kv_heads, c.max_len, start, count, c.kimp_bf16};
+  Kv8ProjectParams p{static_cast<const uint8_t*>(ls.k), ls.k_scale, ls.kimp, ls.wk, ctx->status, ls.kl,
+                     c.n_kv_heads, c.max_len, start, count, c.kimp_bf16, {}};
+  for (int b = 0; b < c.batch; ++b) p.lens[b] = ls.lens[b];
   const dim3 grid((count + 31) / 32, c.n_kv_heads, c.batch);
 #define TB_KV8_PROJ(T, F, DV, DI)                                   \
   if (ls.kv8 == F && c.head_dim == DV && c.d_imp == DI)             \

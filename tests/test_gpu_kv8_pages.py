@@ -7,7 +7,7 @@ import torch
 
 from query_aware_sparse_decode_b200 import tb as TB
 
-from harness import mask_from_sets, sets_from_mask
+from harness import KIMP_REL, kimp_rows, mask_from_sets, sets_from_mask
 from test_gpu_kv8 import DT, MODES, Case, dev
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +74,27 @@ def test_pages_that_hold_no_listed_token_are_not_missed(dtype):
         assert c.ctx.check_status() == 0
         c.check_attention(q, sets, out, lse, f"page {bad}")
         c.table.copy_(good)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_projection_does_not_miss_pages_past_the_length(dtype):
+    """A ragged batch in a table whose unused entries are no pages; a page that holds tokens is missed."""
+    c = Case("int8", dtype, B=2, page=16, max_len=512, D=64, dimp=16)
+    c.append((300, 37))
+    torch.cuda.synchronize()
+    c.table[0, 19:] = -1      # 300 tokens lie on 19 pages, 37 on 3
+    c.table[1, 3:] = 1 << 30
+    c.kimp.fill_(7.0)
+    c.ctx.project_kimp(0, 0, 300)
+    torch.cuda.synchronize()
+    assert c.ctx.check_status() == 0
+    got = kimp_rows(c.kimp)
+    for b, L in enumerate(c.lens):
+        k = c.val["k"][b, :, :L]
+        assert np.all(np.abs(got[b, :, :L] - k @ c.W) <= KIMP_REL * (np.abs(k) @ np.abs(c.W)) + 1e-30)
+    assert np.all(got[1, :, 48:300] == 0) and np.all(got[:, :, 300:] == 7.0)
+    c.table[1, 1] = -1
+    c.ctx.project_kimp(0, 0, 300)
+    torch.cuda.synchronize()
+    assert c.ctx.check_status() == 1
+    assert np.all(kimp_rows(c.kimp)[1, :, 16:32] == 0)
