@@ -188,7 +188,8 @@ TB_API tb_status tb_bind_layer_paged(tb_ctx* ctx, int layer, void* k_pool, void*
  * Every call works on such layers, and a context may mix them with others.  In
  * the attention over bf16 queries a token's weight (softmax numerator times V
  * scale) keeps 11 bits down to 2^-25 of the largest of its head and vanishes
- * below 2^-36 of it; sums are fp32.  Logits may have any size that fp32 holds.
+ * below 2^-36 of it; where the V scales are not powers of two it is off by up to
+ * 2^-14 of itself besides.  Sums are fp32.  Logits may have any size that fp32 holds.
  * Lengths start at 0. */
 #define TB_KV8_BLOCK 16
 typedef enum { TB_KV8_E4M3 = 1, TB_KV8_INT8 = 2 } tb_kv8_format;

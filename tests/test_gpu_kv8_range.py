@@ -110,3 +110,42 @@ def test_large_queries_beside_large_scales(fmt, dtype, mode):
             ref += p / p.sum()
             slack = max(slack, 72 * 2.0 ** -24 * float((np.abs(c.val["k"][0, 0, :90]) @ np.abs(host(q)[0, h])).max()) / 8.0)
         assert np.all(np.abs(host(votes)[0, :90] - ref) <= (2 * slack + 4e-6) * ref + 1e-30)
+
+
+@pytest.mark.parametrize("mode", ["head", "dense"])
+@pytest.mark.parametrize("spread", [0, 30, 70])
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("int8", "bf16"), ("int8", "f32")])
+def test_scales_that_are_not_powers_of_two(fmt, dtype, spread, mode):
+    """Caches that another program quantised: any positive finite scales.  log2 of a V scale is off by at most 3 units
+    of its last place (2^-16 for |log2| in [64, 128)), its sums with the references by half a step each: a weight is off
+    by less than 2^-14 of itself, beside the rest."""
+    c = Case(fmt, dtype, B=2, Hq=8, Hkv=2, max_len=512, seed=spread)
+    c.append((300, 37))
+    torch.cuda.synchronize()
+    for x, t, up in (("k", c.ks, 0), ("v", c.vs, spread)):
+        f = c.rng.uniform(1, 2, size=t.shape) * np.exp2(c.rng.integers(-up, up + 1, size=t.shape))
+        t.copy_(torch.from_numpy(host(t) * f).float())
+        codes, s = c.cached()["kv".index(x)]
+        c.val[x] = codes * np.repeat(s, 16, axis=2)[..., None]
+    q = dev(c.rng.normal(size=(2, 8, c.D)), dtype)
+    sets, mask = c.all_tokens(), None
+    if mode == "head":
+        sets = random_sets(c, c.Hq, 0.4, empty={(1, 0)})
+        mask = mask_from_sets(sets, 2, c.Hq, c.max_len)
+    out, lse = torch.zeros((2, 8, c.D), dtype=DT[dtype], device="cuda"), torch.zeros((2, 8), device="cuda")
+    c.ctx.sparse_attn(0, q, mask, MODES[mode], out, lse)
+    ko, vo = (torch.zeros((2, 2, 300, c.D), dtype=DT[dtype], device="cuda") for _ in range(2))
+    c.ctx.read_kv(0, 0, 300, ko, vo)
+    torch.cuda.synchronize()
+    half, w = (2.0 ** -8, 2.0 ** -11) if dtype == "bf16" else (2.0 ** -24, 0.0)
+    for b in range(2):
+        for h in range(8):
+            o, z, weight, dot = O8.attend(host(q)[b, h], c.val["k"][b, h // c.gs], c.val["v"][b, h // c.gs], sets[b, h])
+            dl = (c.D + 8) * 2.0 ** -24 * dot / math.sqrt(c.D)
+            tol = half * np.abs(o) + (w + 2.0 ** -14 + 2 * dl + 1e-5) * weight + 1e-36
+            assert np.all(np.abs(host(out)[b, h] - o) <= tol), f"b{b} h{h}"
+            got = float(lse[b, h])
+            assert got == z if z == -math.inf else abs(got - z) <= dl + 2e-6 * (1 + abs(z)), f"lse b{b} h{h}"
+        L = c.lens[b]
+        for x, t in (("k", ko), ("v", vo)):
+            assert np.all(np.abs(host(t)[b, :, :L] - c.val[x][b, :, :L]) <= half * np.abs(c.val[x][b, :, :L]))
