@@ -57,7 +57,10 @@ __device__ __forceinline__ void write_output(const AttnKv8Params& p, int b, int 
 // sequence has: the shortest chunks (whole mask words) that keep the call's CTAs
 // within one wave of kKv8CtasPerSm per SM, or, where these would be longer than
 // `long_chunk`, within as many waves as bring them down to it.  A batch with more
-// (sequence, KV head) pairs than one wave has CTAs takes chunks of long_chunk.
+// (sequence, KV head) pairs than these waves have CTAs takes chunks of long_chunk, whatever
+// its lengths are: a long sequence among many short ones is then on few CTAs (8 KV heads, 127
+// sequences of 100 tokens and one of 32768: dense 66 us, one set per KV group 75 us; the long
+// one alone 17 and 14 us).
 //  - Every token: 2048 (B = 4, L = 131072: 163 us, 203 us in one wave of 7296, 173 us with 512).
 //  - Lists: 8192, since a CTA's first tile waits for a chain of mask, row and scale
 //    loads and a sparse chunk has few tiles (the same lengths, one set per KV group with
@@ -388,8 +391,8 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // without ldmatrix or shuffles:
 //  - K: lane (grp, tq) takes 16-byte pieces of rows grp and grp + 8; a word
 //    (4 dims) is one k-step's share of a lane (fp8 mma.sync would take the codes as they
-//    are, but sm_100a expands it into the same conversions: 557 instructions a tile
-//    instead of 398);
+//    are, but sm_100a expands it into the same conversions: in this kernel's form of that
+//    time 557 instructions a tile instead of 398);
 //  - V: it takes D/8 bytes (dims grp D/8 ..) of token rows 2tq, 2tq+1, 2tq+8,
 //    2tq+9; byte permutes pair the tokens of a dim, and m-tile mt takes dims
 //    grp D/8 + 2mt and + 2mt + 1 as its rows grp and grp + 8.
@@ -418,9 +421,10 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 // passed fp16 above |x| = 2^26 or so, where the step of x exceeds the 4.)
 //
 // Measured with the combine (32 / 8 heads, D = 128, e4m3, L = 131072, B = 4): every
-// token 166 us, 6.5 TB/s, the copy peak; 30 % per head 132 us, 6.2 TB/s (gathered 128-byte
-// rows); one set of 30 % per KV group 62 us, 5.2 TB/s.  int8 takes 3 to 10 % longer (454
-// instructions a tile against 357: its widening has no instruction of its own).
+// token 167 us, 6.5 TB/s, the copy peak; 30 % per head 133 us, 6.2 TB/s (gathered 128-byte
+// rows); one set of 30 % per KV group 65 us, 5.0 TB/s.  int8 takes 2 % longer for every token
+// and 10 to 17 % for sets (434 instructions a tile against 340: its widening has no
+// instruction of its own).
 template <int FMT, int D, int GS, bool DENSE>
 __global__ void __launch_bounds__(kAttnThreads, kKv8CtasPerSm) attn_kv8_kernel(const AttnKv8Params p) {
   pdl_wait();
@@ -797,7 +801,8 @@ struct VoteKv8Params : VoteParams {
 // keys; softvote_reduce_kernel follows.  S^T = K Q^T as in attn_kv8_kernel, over
 // consecutive tokens: a tile of 16 is one block of the cache, so it has one
 // scale and one row lookup.  A ring of kVoteKv8Stages tiles per warp.  Measured (B = 1, L =
-// 131072): 25 us of the call's 34 us, 5.3 TB/s, over half of the issue slots used.
+// 131072): 25 us of the call's 34 us, 5.3 TB/s; no unit is full (cold, 27 us: 58 % of the
+// issue slots, ALU 47 %, DRAM cycles 63 %).
 constexpr int kVoteKv8Stages = 3;
 template <int D>
 constexpr int vote_kv8_smem() { return kVoteWarps * kVoteKv8Stages * (kAttnTile * D + 16); }

@@ -41,8 +41,8 @@ __device__ __forceinline__ uint32_t kv_row(const KvLayout& kl, int b, int g, int
   return ((uint32_t)page * Hkv + g) * (uint32_t)kl.page_size + (uint32_t)(t & (kl.page_size - 1));
 }
 // kv_row with the page id checked against the pool; false: not a page of it.
-__host__ __device__ __forceinline__ bool kv_row_checked(const KvLayout& kl, int b, int g, int Hkv, int max_len,
-                                                        int t, uint32_t* row) {
+__device__ __forceinline__ bool kv_row_checked(const KvLayout& kl, int b, int g, int Hkv, int max_len, int t,
+                                               uint32_t* row) {
   if (kl.page_table == nullptr) {
     *row = ((uint32_t)b * Hkv + g) * (uint32_t)max_len + (uint32_t)t;
     return true;
